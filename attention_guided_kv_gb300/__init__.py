@@ -45,6 +45,17 @@ class PagedKV(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
+class PagedKV4(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class ScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int32),
+                ("n_sink", ctypes.c_int32)]
+
+
 class BpOptions(ctypes.Structure):
     _fields_ = [("update", ctypes.c_int), ("history", ctypes.c_void_p), ("window", ctypes.c_int),
                 ("step", ctypes.c_int64), ("history_tokens", ctypes.c_int64), ("threshold", ctypes.c_float)]
@@ -62,6 +73,7 @@ class SnapOptions(ctypes.Structure):
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _PKV = ctypes.POINTER(PagedKV)
+_PKV4 = ctypes.POINTER(PagedKV4)
 
 # name -> (restype, argtypes)
 _SIGS = {
@@ -101,6 +113,14 @@ _SIGS = {
     "kvsel_quest_decode_workspace": (_sz, [_PKV, _i, _i, _i, _i, _i]),
     "kvsel_quest_decode": (_i, [_PKV, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _f, _vp, _i, _vp, _vp, _vp, _sz,
                                 _vp]),
+    "kvsel_kv4_append_workspace": (_sz, [_PKV4, _i]),
+    "kvsel_kv4_append": (_i, [_PKV4, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+    "kvsel_kv4_read": (_i, [_PKV4, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "kvsel_kv4_decode_attn_workspace": (_sz, [_PKV4, _i, _i, _i, _i]),
+    "kvsel_kv4_decode_attn": (_i, [_PKV4, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _f, ctypes.POINTER(ScoreMod),
+                                   _vp, _i, _vp, _vp, _i, _vp, _sz, _vp]),
+    "kvsel_kv4_evict_workspace": (_sz, [_PKV4, _i, _i]),
+    "kvsel_kv4_evict": (_i, [_PKV4, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "kvsel_snapkv_select_ex": (_i, [_PKV, _vp, _i, _i, _i, _vp, _i, _f, _i, _i, ctypes.POINTER(SnapOptions), _vp,
                                     _vp, _vp, _sz, _vp]),
 }
@@ -526,3 +546,183 @@ def kvsel_quest_decode(kv: PagedKV, block_table, seq_lens, q, page_meta, out, wo
         _ptr(k_new), _ptr(v_new), _ptr(page_meta), int(budget_pages), float(scale), _ptr(out),
         KVSEL_F32 if out.dtype == torch.float32 else KVSEL_BF16, _ptr(pages_out), _ptr(bounds_out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# the paged 4-bit cache
+# ----------------------------------------------------------------------------
+def _shaped(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}")
+
+
+def paged_kv4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+              num_q_heads: int) -> PagedKV4:
+    """Descriptor of a 4-bit cache: codes uint8 [num_pages][num_kv_heads][page_size][64], scales bf16
+    [num_pages][num_kv_heads][page_size][4][2] ({scale, minimum} of each group of 32 values)."""
+    for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _need(t, torch.uint8, name)
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _need(t, torch.bfloat16, name)
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [pages][Hkv][page][head_dim / 2]")
+    P, H, pg, half = k_codes.shape
+    _shaped(v_codes, k_codes.shape, "v_codes")
+    _shaped(k_scales, (P, H, pg, half // 16, 2), "k_scales")
+    _shaped(v_scales, (P, H, pg, half // 16, 2), "v_scales")
+    _same_device(k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
+    return PagedKV4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), P, H, num_q_heads,
+                    2 * half, pg)
+
+
+def _table_of(block_table, seq_lens):
+    _need(block_table, torch.int32, "block_table")
+    _need(seq_lens, torch.int32, "seq_lens")
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table must be [batch][max_pages] and seq_lens [batch]")
+    return seq_lens.shape[0]
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _per_slot(kv, batch, max_len, **tensors):
+    """The common row length of the given [batch][num_kv_heads][max_len] tensors (0 without any)."""
+    for name, t in tensors.items():
+        if t is not None:
+            max_len = t.shape[-1] if max_len is None else max_len
+            _shaped(t, (batch, kv.num_kv_heads, max_len), name)
+    return max_len
+
+
+def kvsel_kv4_append_workspace(kv: PagedKV4, batch: int) -> int:
+    return int(lib().kvsel_kv4_append_workspace(ctypes.byref(kv), int(batch)))
+
+
+def kvsel_kv4_append(kv: PagedKV4, block_table, seq_lens, tok_off, k, v, workspace, *, pos_map=None, next_pos=None,
+                     h2o_cum=None, stream=None):
+    """Quantise packed new tokens (k, v bf16 [total][Hkv][128]; sequence b's are rows tok_off[b]..tok_off[b + 1])
+    into the cache behind each sequence's live ones; seq_lens (and next_pos) grow."""
+    batch = _table_of(block_table, seq_lens)
+    _need(tok_off, torch.int32, "tok_off")
+    _shaped(tok_off, (batch + 1,), "tok_off")
+    _need(k, torch.bfloat16, "k")
+    _need(v, torch.bfloat16, "v")
+    _shaped(k, (k.shape[0], kv.num_kv_heads, kv.head_dim), "k")
+    _shaped(v, k.shape, "v")
+    _need(pos_map, torch.int32, "pos_map", True)
+    _need(next_pos, torch.int32, "next_pos", True)
+    _shaped(next_pos, (batch,), "next_pos")
+    _need(h2o_cum, torch.float32, "h2o_cum", True)
+    _need(workspace, workspace.dtype, "workspace")
+    max_len = _per_slot(kv, batch, None, pos_map=pos_map, h2o_cum=h2o_cum) or 0
+    _same_device(block_table, seq_lens=seq_lens, tok_off=tok_off, k=k, v=v, pos_map=pos_map, next_pos=next_pos,
+                 h2o_cum=h2o_cum, workspace=workspace)
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvsel_kv4_append(
+            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(tok_off), k.shape[0],
+            _ptr(k), _ptr(v), _ptr(pos_map), _ptr(next_pos), _ptr(h2o_cum), max_len, _ptr(workspace), _nbytes(workspace),
+            _stream(stream)))
+
+
+def kvsel_kv4_read(kv: PagedKV4, block_table, seq_lens, tok_off, k_out, v_out, workspace, *, start=None, stream=None):
+    """Read cached tokens back as bf16: packed row tok_off[b] + i is slot start[b] + i (or i) of sequence b."""
+    batch = _table_of(block_table, seq_lens)
+    _need(tok_off, torch.int32, "tok_off")
+    _shaped(tok_off, (batch + 1,), "tok_off")
+    _need(start, torch.int32, "start", True)
+    _shaped(start, (batch,), "start")
+    _need(k_out, torch.bfloat16, "k_out")
+    _need(v_out, torch.bfloat16, "v_out")
+    _shaped(k_out, (k_out.shape[0], kv.num_kv_heads, kv.head_dim), "k_out")
+    _shaped(v_out, k_out.shape, "v_out")
+    _need(workspace, workspace.dtype, "workspace")
+    _same_device(block_table, seq_lens=seq_lens, tok_off=tok_off, start=start, k_out=k_out, v_out=v_out,
+                 workspace=workspace)
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvsel_kv4_read(
+            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(tok_off),
+            k_out.shape[0], _ptr(start), _ptr(k_out), _ptr(v_out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def kvsel_kv4_decode_attn_workspace(kv: PagedKV4, batch: int, max_len: int, with_probs: bool, with_cum: bool) -> int:
+    return int(lib().kvsel_kv4_decode_attn_workspace(ctypes.byref(kv), int(batch), int(max_len), int(bool(with_probs)),
+                                                     int(bool(with_cum))))
+
+
+def kvsel_kv4_decode_attn(kv: PagedKV4, block_table, seq_lens, q, out, workspace, *, k_new=None, v_new=None,
+                          pos_map=None, next_pos=None, scale=None, softcap=0.0, slopes=None, window=0, n_sink=0,
+                          probs=None, h2o_cum=None, max_len=None, stream=None):
+    """Append (optional) + decode attention over the 4-bit cache + probabilities + H2O score update.
+
+    softcap: scores become softcap * tanh(score / softcap).  slopes (fp32 [num_q_heads]): slopes[h] times the
+    distance is taken off the score.  window: only the last `window` positions and the first `n_sink` are seen.
+    Positions are pos_map's where it is given, else the slots.
+    """
+    batch = _table_of(block_table, seq_lens)
+    _need(q, torch.bfloat16, "q")
+    _shaped(q, (batch, kv.num_q_heads, kv.head_dim), "q")
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _need(t, torch.bfloat16, name, True)
+        _shaped(t, (batch, kv.num_kv_heads, kv.head_dim), name)
+    _need(pos_map, torch.int32, "pos_map", True)
+    _need(next_pos, torch.int32, "next_pos", True)
+    _shaped(next_pos, (batch,), "next_pos")
+    _need(slopes, torch.float32, "slopes", True)
+    _shaped(slopes, (kv.num_q_heads,), "slopes")
+    _need(probs, torch.float32, "probs", True)
+    _need(h2o_cum, torch.float32, "h2o_cum", True)
+    _need(workspace, workspace.dtype, "workspace")
+    if out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous() or out.device.type != "cuda":
+        raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor")
+    _shaped(out, q.shape, "out")
+    if max_len is None and probs is not None:
+        max_len = probs.shape[-1]
+    max_len = _per_slot(kv, batch, max_len, pos_map=pos_map, h2o_cum=h2o_cum)
+    if max_len is None:
+        max_len = block_table.shape[1] * kv.page_size
+    _shaped(probs, (batch, kv.num_q_heads, max_len), "probs")
+    _same_device(block_table, seq_lens=seq_lens, q=q, out=out, k_new=k_new, v_new=v_new, pos_map=pos_map,
+                 next_pos=next_pos, slopes=slopes, probs=probs, h2o_cum=h2o_cum, workspace=workspace)
+    mod = None
+    if softcap != 0 or slopes is not None or window != 0 or n_sink != 0:
+        mod = ScoreMod(float(softcap), slopes.data_ptr() if slopes is not None else None, int(window), int(n_sink))
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvsel_kv4_decode_attn(
+            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(q), _ptr(k_new),
+            _ptr(v_new), _ptr(pos_map), _ptr(next_pos), float(kv.head_dim ** -0.5 if scale is None else scale),
+            ctypes.byref(mod) if mod is not None else None, _ptr(out),
+            KVSEL_F32 if out.dtype == torch.float32 else KVSEL_BF16, _ptr(probs), _ptr(h2o_cum), int(max_len),
+            _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def kvsel_kv4_evict_workspace(kv: PagedKV4, batch: int, budget: int) -> int:
+    return int(lib().kvsel_kv4_evict_workspace(ctypes.byref(kv), int(batch), int(budget)))
+
+
+def kvsel_kv4_evict(kv: PagedKV4, block_table, seq_lens, h2o_cum, workspace, *, budget, n_sink, window, compact=False,
+                    pos_map=None, keep_out=None, freed_pages=None, stream=None):
+    """kvsel_h2o_evict for the 4-bit cache: select by accumulated weight; optional in-place compaction."""
+    batch = _table_of(block_table, seq_lens)
+    _need(h2o_cum, torch.float32, "h2o_cum")
+    _need(pos_map, torch.int32, "pos_map", True)
+    _need(keep_out, torch.int32, "keep_out", True)
+    _shaped(keep_out, (batch, kv.num_kv_heads, int(budget)), "keep_out")
+    _need(freed_pages, torch.int32, "freed_pages", True)
+    _shaped(freed_pages, block_table.shape, "freed_pages")
+    _need(workspace, workspace.dtype, "workspace")
+    max_len = _per_slot(kv, batch, None, h2o_cum=h2o_cum, pos_map=pos_map)
+    _same_device(block_table, seq_lens=seq_lens, h2o_cum=h2o_cum, pos_map=pos_map, keep_out=keep_out,
+                 freed_pages=freed_pages, workspace=workspace)
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvsel_kv4_evict(
+            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(h2o_cum), _ptr(pos_map),
+            max_len, int(budget), int(n_sink), int(window), int(bool(compact)), _ptr(keep_out), _ptr(freed_pages),
+            _ptr(workspace), _nbytes(workspace), _stream(stream)))

@@ -23,6 +23,7 @@
 //   ceil(n_keep / page_size) and publishes the new length.
 #include "common.cuh"
 #include "h2o_link.cuh"
+#include "h2o_select.cuh"
 #include "row_topk.cuh"
 
 namespace kvsel {
@@ -429,7 +430,68 @@ EvictWs evict_ws_layout(int batch, int Hkv, int budget) {
   w.total = off;
   return w;
 }
+
+// A launch that may begin while its predecessor on the stream drains (the
+// kernels wait for it before they read what it wrote).
+cudaLaunchConfig_t pdl_config(dim3 grid, int threads, size_t smem, cudaLaunchAttribute* attr, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 }  // namespace
+
+kvsel_status kvsel_host::launch_h2o_select(const char* fn, const H2OSelectArgs& a, cudaStream_t st) {
+  SelectParams P;
+  P.seq_lens = a.seq_lens;
+  P.cum = a.cum;
+  P.pos_map = a.pos_map;
+  P.keep_slots = a.keep_slots;
+  P.keep_out = a.keep_out;
+  P.first_move = a.first_move;
+  P.link = a.link;
+  P.status = a.status;
+  P.Hkv = a.num_kv_heads;
+  P.max_len = a.max_len;
+  P.budget = a.budget;
+  P.n_sink = a.n_sink;
+  P.window = a.window;
+  const std::string name(fn);
+  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(h2o_select_kernel), int(sizeof(SelSmem)));
+      e != cudaSuccess)
+    return cuda_fail(e, (name + " (attribute)").c_str());
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(a.num_kv_heads, a.batch), kSelThreads, sizeof(SelSmem), attr, st);
+  trace_before("h2o_select", st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, h2o_select_kernel, P);
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, (name + " (select launch)").c_str());
+  return KVSEL_OK;
+}
+
+kvsel_status kvsel_host::launch_h2o_truncate(const char* fn, const H2OTruncateArgs& a, cudaStream_t st) {
+  TruncateParams T;
+  T.seq_lens = a.seq_lens;
+  T.block_table = a.block_table;
+  T.freed = a.freed;
+  T.max_pages = a.max_pages;
+  T.budget = a.budget;
+  T.max_len = a.max_len;
+  T.page_shift = a.page_shift;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(a.batch), 256, 0, attr, st);
+  trace_before("h2o_truncate", st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, h2o_truncate_kernel, T);
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, (std::string(fn) + " (truncate launch)").c_str());
+  return KVSEL_OK;
+}
 
 extern "C" kvsel_status kvsel_h2o_link_reset(void* workspace, int batch, int num_kv_heads, void* stream) {
   const std::string fn = "kvsel_h2o_link_reset: ";
@@ -479,77 +541,55 @@ extern "C" kvsel_status kvsel_h2o_evict(const kvsel_paged_kv* kv, int32_t* block
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  SelectParams P;
-  P.seq_lens = seq_lens;
-  P.cum = h2o_cum;
-  P.pos_map = pos_map;
-  P.keep_slots = reinterpret_cast<int32_t*>(ws + L.keep_off);
-  P.keep_out = keep_out;
-  P.first_move = reinterpret_cast<int32_t*>(ws + L.first_off);
-  P.link = link_layout(workspace, batch * kv->num_kv_heads);
-  P.status = reinterpret_cast<int*>(ws);
-  P.Hkv = kv->num_kv_heads;
-  P.max_len = max_len;
-  P.budget = budget;
-  P.n_sink = n_sink;
-  P.window = window;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kv->num_kv_heads, batch);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelSmem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaError_t a = smem_limit_once(reinterpret_cast<const void*>(h2o_select_kernel), int(sizeof(SelSmem)));
-      a != cudaSuccess)
-    return cuda_fail(a, "kvsel_h2o_evict (attribute)");
-  trace_before("h2o_select", st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, h2o_select_kernel, P);
-  trace_after(st);
-  if (e != cudaSuccess) return cuda_fail(e, "kvsel_h2o_evict (select launch)");
+  H2OSelectArgs A;
+  A.seq_lens = seq_lens;
+  A.cum = h2o_cum;
+  A.pos_map = pos_map;
+  A.keep_slots = reinterpret_cast<int32_t*>(ws + L.keep_off);
+  A.keep_out = keep_out;
+  A.first_move = reinterpret_cast<int32_t*>(ws + L.first_off);
+  A.link = link_layout(workspace, batch * kv->num_kv_heads);
+  A.status = reinterpret_cast<int*>(ws);
+  A.batch = batch;
+  A.num_kv_heads = kv->num_kv_heads;
+  A.max_len = max_len;
+  A.budget = budget;
+  A.n_sink = n_sink;
+  A.window = window;
+  if (kvsel_status s = launch_h2o_select("kvsel_h2o_evict", A, st); s != KVSEL_OK) return s;
   if (!compact) return KVSEL_OK;
 
   CompactParams C;
   C.seq_lens = seq_lens;
   C.block_table = block_table;
-  C.keep_slots = P.keep_slots;
-  C.first_move = P.first_move;
+  C.keep_slots = A.keep_slots;
+  C.first_move = A.first_move;
   C.k_pool = static_cast<__nv_bfloat16*>(kv->k_pool);
   C.v_pool = static_cast<__nv_bfloat16*>(kv->v_pool);
   C.cum = h2o_cum;
   C.pos_map = pos_map;
-  C.status = P.status;
+  C.status = A.status;
   C.Hkv = kv->num_kv_heads;
   C.max_len = max_len;
   C.max_pages = max_pages;
   C.num_pages = kv->num_pages;
   C.budget = budget;
   C.page_shift = page_shift_of(kv->page_size);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3(kv->num_kv_heads, batch), 256, 0, attr, st);
   trace_before("h2o_compact", st);
-  cfg.gridDim = dim3(kv->num_kv_heads, batch);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, h2o_compact_kernel, C);  // programmatic serialization, like the select
+  cudaError_t e = cudaLaunchKernelEx(&cfg, h2o_compact_kernel, C);  // programmatic serialization, like the select
   trace_after(st);
   if (e != cudaSuccess) return cuda_fail(e, "kvsel_h2o_evict (compact launch)");
 
-  TruncateParams T;
+  H2OTruncateArgs T;
   T.seq_lens = seq_lens;
   T.block_table = block_table;
   T.freed = freed_pages;
+  T.batch = batch;
   T.max_pages = max_pages;
   T.budget = budget;
   T.max_len = max_len;
   T.page_shift = C.page_shift;
-  trace_before("h2o_truncate", st);
-  cfg.gridDim = dim3(batch);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, h2o_truncate_kernel, T);
-  trace_after(st);
-  if (e != cudaSuccess) return cuda_fail(e, "kvsel_h2o_evict (truncate launch)");
-  return KVSEL_OK;
+  return launch_h2o_truncate("kvsel_h2o_evict", T, st);
 }

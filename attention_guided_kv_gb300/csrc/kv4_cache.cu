@@ -1,0 +1,492 @@
+// The paged 4-bit KV cache: append (quantise), read back, and H2O eviction
+// with in-place compaction (sm_103a).  The number format is in kv4.cuh.
+//
+// append kernel: 16 neighbouring threads take one row (token, kv head), eight
+//   values of K and eight of V each: one 16-byte load a side, the group's
+//   minimum and maximum over four lanes by shuffles, one 4-byte store of codes
+//   a side and, from one lane in four, one of {scale, minimum}.  Nothing is
+//   read twice and every store is part of a full 64-byte row.  Bound by HBM:
+//   512 bytes read and 160 written a row.
+// read kernel: the inverse, 160 bytes read and 512 written a row.
+// evict: the select of h2o_evict.cu, then one cluster of 8 CTAs per
+//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 448
+//   kept rows in the cluster's shared memory, waits for the whole cluster and
+//   writes them to their new slots; kept lists are ascending, so keep[i] >= i
+//   and a round never writes a slot that a later round still reads.  One
+//   barrier per round is the only ordering; a CTA per row, as the bf16
+//   cache's compaction has it, leaves most SMs idle at 64 rows.
+#include "common.cuh"
+#include "h2o_select.cuh"
+#include "kv4.cuh"
+
+namespace kvsel {
+
+constexpr int kQaThreads = 256;
+constexpr int kQaRows = kQaThreads / 16;  // (token, kv head) rows a CTA takes at a time
+
+struct Kv4Params {
+  uint8_t* codes[2];   // K, V
+  uint8_t* scales[2];
+  const int32_t* block_table;
+  int32_t* seq_lens;
+  const int32_t* tok_off;
+  int* status;
+  uint32_t* ticket;    // workspace: CTAs that are done with seq_lens
+  int Hkv, max_pages, num_pages, page_lg, batch;
+  int total;           // packed tokens
+};
+
+struct AppendParams : Kv4Params {
+  const uint4* k;
+  const uint4* v;
+  int32_t* pos_map;
+  int32_t* next_pos;
+  float* cum;
+  int max_len;
+};
+
+struct ReadParams : Kv4Params {
+  const int32_t* start;
+  uint4* k;
+  uint4* v;
+};
+
+// The sequence that owns packed token t: the last b with tok_off[b] <= t.
+__device__ __forceinline__ int owner_of(const int32_t* off, int batch, int t) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(off + mid) <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Run length of sequence b, or -1 if the offsets are not 0 <= ... <= total.
+__device__ __forceinline__ int run_of(const Kv4Params& P, int b) {
+  const int a = __ldg(P.tok_off + b), e = __ldg(P.tok_off + b + 1);
+  return a >= 0 && e >= a && e <= P.total ? e - a : -1;
+}
+
+__global__ void __launch_bounds__(kQaThreads) kv4_append_kernel(const AppendParams P) {
+  const int tid = threadIdx.x, l16 = tid & 15;
+  const long long rows = (long long)P.total * P.Hkv;
+  const int page_mask = (1 << P.page_lg) - 1;
+  const long long capacity = (long long)P.max_pages << P.page_lg;
+#pragma unroll 1
+  for (long long r0 = (long long)blockIdx.x * kQaRows; r0 < rows; r0 += (long long)gridDim.x * kQaRows) {
+    const long long r = r0 + (tid >> 4);
+    const bool in = r < rows;
+    const long long rc = in ? r : rows - 1;   // every lane takes part in the shuffles
+    const uint4 kx = __ldcs(P.k + rc * 16 + l16), vx = __ldcs(P.v + rc * 16 + l16);
+    const int t = int(rc / P.Hkv), g = int(rc - (long long)t * P.Hkv);
+    const int b = owner_of(P.tok_off, P.batch, t);
+    const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
+    const int S = __ldcg(P.seq_lens + b);
+    bool ok = n >= 0 && at >= 0 && at < n && S >= 0 && (long long)S + n <= capacity &&
+              (P.max_len == 0 || (long long)S + n <= P.max_len);
+    long long row = 0;
+    const int slot = S + at;
+    if (ok) {
+      const int phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
+      ok = unsigned(phys) < unsigned(P.num_pages);
+      row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+    }
+    const bool tail = t >= __ldg(P.tok_off + P.batch);  // rows behind the last sequence are nobody's
+    if (in && !ok && !tail && l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+    uint32_t sz[2], codes[2];
+    const uint32_t kr[4] = {kx.x, kx.y, kx.z, kx.w}, vr[4] = {vx.x, vx.y, vx.z, vx.w};
+    codes[0] = q4_group<8>(kr, sz[0]);
+    codes[1] = q4_group<8>(vr, sz[1]);
+    if (!in || !ok) continue;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      reinterpret_cast<uint32_t*>(P.codes[side] + row * kQ4CodeBytes)[l16] = codes[side];
+      if ((l16 & 3) == 0) reinterpret_cast<uint32_t*>(P.scales[side] + row * kQ4ScaleBytes)[l16 >> 2] = sz[side];
+    }
+    if (l16 == 0) {
+      const size_t at_row = ((size_t)b * P.Hkv + g) * P.max_len + slot;
+      if (P.pos_map) P.pos_map[at_row] = __ldcg(P.next_pos + b) + at;
+      if (P.cum) P.cum[at_row] = 0.0f;
+    }
+  }
+  // the lengths change once every CTA has read them
+  __shared__ bool last;
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(P.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int b = tid; b < P.batch; b += kQaThreads) {
+    const int n = run_of(P, b), S = __ldcg(P.seq_lens + b);
+    if (n < 0 || S < 0 || (long long)S + n > capacity || (P.max_len != 0 && (long long)S + n > P.max_len)) {
+      report(P.status, KVSEL_ERR_BAD_INDEX);
+      continue;
+    }
+    P.seq_lens[b] = S + n;
+    if (P.next_pos) P.next_pos[b] = __ldcg(P.next_pos + b) + n;
+  }
+  if (tid == 0) *P.ticket = 0u;
+}
+
+__global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P) {
+  const int tid = threadIdx.x, l16 = tid & 15;
+  const long long rows = (long long)P.total * P.Hkv;
+  const int page_mask = (1 << P.page_lg) - 1;
+  const long long capacity = (long long)P.max_pages << P.page_lg;
+#pragma unroll 1
+  for (long long r = (long long)blockIdx.x * kQaRows + (tid >> 4); r < rows; r += (long long)gridDim.x * kQaRows) {
+    const int t = int(r / P.Hkv), g = int(r - (long long)t * P.Hkv);
+    if (t >= __ldg(P.tok_off + P.batch)) continue;  // rows behind the last sequence stay as they are
+    const int b = owner_of(P.tok_off, P.batch, t);
+    const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
+    const int S = __ldg(P.seq_lens + b), first = P.start ? __ldg(P.start + b) : 0;
+    const long long slot = (long long)first + at;
+    bool ok = n >= 0 && at >= 0 && at < n && first >= 0 && slot < S && slot < capacity;
+    int phys = -1;
+    if (ok) {
+      phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
+      ok = unsigned(phys) < unsigned(P.num_pages);
+    }
+    if (!ok) {
+      if (l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+      continue;
+    }
+    const long long row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+    uint32_t codes[2], sz[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      codes[side] = __ldg(reinterpret_cast<const uint32_t*>(P.codes[side] + row * kQ4CodeBytes) + l16);
+      sz[side] = __ldg(reinterpret_cast<const uint32_t*>(P.scales[side] + row * kQ4ScaleBytes) + (l16 >> 2));
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const float s = bf16lo_to_f32(sz[side]), z = bf16hi_to_f32(sz[side]);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(float((codes[side] >> (4 * i)) & 15u), s, z);
+      const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                 pack_bf16x2(x[6], x[7]));
+      __stcs((side ? P.v : P.k) + r * 16 + l16, o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// compaction
+// ---------------------------------------------------------------------------
+constexpr int kQcCluster = 8;
+constexpr int kQcRows = 448;     // kept rows a CTA stages per round
+constexpr int kQcThreads = 512;
+constexpr int kQcUnits = 10;     // 16-byte units of a row: K codes 4, V codes 4, K and V scales
+
+struct Compact4Params {
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const int32_t* keep_slots;
+  const int32_t* first_move;
+  uint8_t* codes[2];
+  uint8_t* scales[2];
+  float* cum;
+  int32_t* pos_map;
+  int* status;
+  int Hkv, max_len, max_pages, num_pages, budget, page_lg;
+};
+
+struct Compact4Smem {
+  uint4 unit[kQcRows][kQcUnits];
+  long long src[kQcRows], dst[kQcRows];  // pool rows, -1: a bad table entry
+  float cum[kQcRows];
+  int32_t pos[kQcRows];
+};
+
+__global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4Params P) {
+  extern __shared__ __align__(16) uint8_t qc_smem[];
+  Compact4Smem& sm = *reinterpret_cast<Compact4Smem*>(qc_smem);
+  const int rank = blockIdx.x % kQcCluster, kvh = blockIdx.x / kQcCluster, b = blockIdx.y, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept lists come from the select
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
+  const int S = P.seq_lens[b];
+  if (S <= P.budget) return;  // the same for the whole cluster, as below
+  if (S > P.max_len || (long long)S > ((long long)P.max_pages << P.page_lg)) {
+    if (tid == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+    return;
+  }
+  const size_t rowi = size_t(b) * P.Hkv + kvh;
+  const int32_t* keep = P.keep_slots + rowi * P.budget;
+  const int32_t* bt = P.block_table + size_t(b) * P.max_pages;
+  float* crow = P.cum + rowi * P.max_len;
+  int32_t* prow = P.pos_map ? P.pos_map + rowi * P.max_len : nullptr;
+  const int page_mask = (1 << P.page_lg) - 1;
+  auto pool_row = [&](int slot) -> long long {
+    const int phys = bt[slot >> P.page_lg];
+    if (unsigned(phys) >= unsigned(P.num_pages)) {
+      report(P.status, KVSEL_ERR_BAD_INDEX);
+      return -1;
+    }
+    return (((long long)phys * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);
+  };
+#pragma unroll 1
+  for (int c0 = P.first_move[rowi]; c0 < P.budget; c0 += kQcCluster * kQcRows) {
+    // an even share of the round's rows for every CTA of the cluster
+    const int left = min(kQcCluster * kQcRows, P.budget - c0);
+    const int share = (left + kQcCluster - 1) / kQcCluster;
+    const int i0 = c0 + rank * share, cnt = max(0, min(share, left - rank * share));
+    for (int i = tid; i < cnt; i += kQcThreads) {
+      const int src = keep[i0 + i];
+      sm.src[i] = pool_row(src);
+      sm.dst[i] = pool_row(i0 + i);
+      sm.cum[i] = crow[src];
+      if (prow) sm.pos[i] = prow[src];
+    }
+    __syncthreads();
+    for (int u = tid; u < cnt * kQcUnits; u += kQcThreads) {
+      const int i = u / kQcUnits, w = u - i * kQcUnits;
+      const long long row = sm.src[i];
+      if (row < 0) continue;
+      const uint8_t* from = w < 8 ? P.codes[w >> 2] + row * kQ4CodeBytes + (w & 3) * 16 : P.scales[w - 8] + row * kQ4ScaleBytes;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[i][w])), "l"(from) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // all of the round's sources are in shared memory before any of its slots is written
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int u = tid; u < cnt * kQcUnits; u += kQcThreads) {
+      const int i = u / kQcUnits, w = u - i * kQcUnits;
+      const long long row = sm.dst[i];
+      if (row < 0 || sm.src[i] < 0) continue;
+      uint8_t* to = w < 8 ? P.codes[w >> 2] + row * kQ4CodeBytes + (w & 3) * 16 : P.scales[w - 8] + row * kQ4ScaleBytes;
+      *reinterpret_cast<uint4*>(to) = sm.unit[i][w];
+    }
+    for (int i = tid; i < cnt; i += kQcThreads) {
+      crow[i0 + i] = sm.cum[i];
+      if (prow) prow[i0 + i] = sm.pos[i];
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace kvsel
+
+using namespace kvsel;
+using namespace kvsel_host;
+
+namespace {
+
+kvsel_status check_kv4(const std::string& fn, const kvsel_paged_kv4* kv) {
+  if (!kv || kv->num_kv_heads < 1 || kv->num_pages < 1)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "a cache descriptor with num_pages, num_kv_heads >= 1 is required");
+  if (!kv->k_codes || !kv->v_codes || !kv->k_scales || !kv->v_scales)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "k_codes, v_codes, k_scales and v_scales are required");
+  for (const void* p : {kv->k_codes, kv->v_codes, kv->k_scales, kv->v_scales})
+    if (!aligned(p, 16)) return fail(KVSEL_ERR_INVALID_ARG, fn + "pools must be 16-byte aligned");
+  if (page_shift_of(kv->page_size) < 0 || kv->head_dim != kQ4D)
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "only head_dim 128 and page_size 16, 32, 64, 128 or 256 are implemented");
+  return KVSEL_OK;
+}
+
+void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages, int32_t* seq_lens, int batch,
+          const int32_t* tok_off, int total, void* workspace) {
+  P.codes[0] = static_cast<uint8_t*>(kv->k_codes);
+  P.codes[1] = static_cast<uint8_t*>(kv->v_codes);
+  P.scales[0] = static_cast<uint8_t*>(kv->k_scales);
+  P.scales[1] = static_cast<uint8_t*>(kv->v_scales);
+  P.block_table = block_table;
+  P.seq_lens = seq_lens;
+  P.tok_off = tok_off;
+  P.status = static_cast<int*>(workspace);
+  P.ticket = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  P.Hkv = kv->num_kv_heads;
+  P.max_pages = max_pages;
+  P.num_pages = kv->num_pages;
+  P.page_lg = 4 + page_shift_of(kv->page_size);
+  P.batch = batch;
+  P.total = total;
+}
+
+// One CTA per kQaRows rows up to 8 CTAs an SM; more rows are strided over.
+int row_grid(long long rows) {
+  const long long want = (rows + kQaRows - 1) / kQaRows, most = (long long)sm_count() * 8;
+  return int(want < most ? want : most);
+}
+
+struct Evict4Ws {
+  H2OLink link;
+  size_t link_off, keep_off, first_off, total;
+};
+// The status block, then the thresholds and candidate counts of the select
+// (no candidate lists: the 4-bit decode step does not collect any), the kept
+// slots and each row's first slot that moves.
+Evict4Ws evict4_layout(int batch, int Hkv, int budget) {
+  Evict4Ws w;
+  const size_t words = align_up(size_t(batch) * Hkv * 4, 256);
+  w.link_off = kStatusBytes;
+  w.keep_off = w.link_off + 2 * words;
+  w.first_off = align_up(w.keep_off + size_t(batch) * Hkv * budget * 4, 256);
+  w.total = w.first_off + words;
+  return w;
+}
+
+}  // namespace
+
+extern "C" size_t kvsel_kv4_append_workspace(const kvsel_paged_kv4* kv, int batch) {
+  if (!kv || batch < 1) return 0;
+  return kStatusBytes + 256;
+}
+
+extern "C" kvsel_status kvsel_kv4_append(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                         int32_t* seq_lens, int batch, const int32_t* tok_off, int total_tokens,
+                                         const void* k, const void* v, int32_t* pos_map, int32_t* next_pos,
+                                         float* h2o_cum, int max_len, void* workspace, size_t ws_bytes, void* stream) {
+  const std::string fn = "kvsel_kv4_append: ";
+  if (kvsel_status s = check_kv4(fn, kv); s != KVSEL_OK) return s;
+  if (!block_table || !seq_lens || !tok_off || batch < 1 || max_pages < 1 || total_tokens < 0)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "block_table, seq_lens, tok_off required; batch, max_pages >= 1, total_tokens >= 0");
+  if (pos_map && !next_pos) return fail(KVSEL_ERR_INVALID_ARG, fn + "pos_map needs next_pos");
+  if ((pos_map || h2o_cum) && max_len < 1)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "pos_map and h2o_cum need max_len >= 1");
+  if (total_tokens > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16)))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "k and v (16-byte aligned) are required");
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < kvsel_kv4_append_workspace(kv, batch))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace of kvsel_kv4_append_workspace() bytes is required");
+  if (total_tokens == 0) return KVSEL_OK;
+  AppendParams P;
+  fill(P, kv, block_table, max_pages, seq_lens, batch, tok_off, total_tokens, workspace);
+  P.k = static_cast<const uint4*>(k);
+  P.v = static_cast<const uint4*>(v);
+  P.pos_map = pos_map;
+  P.next_pos = next_pos;
+  P.cum = h2o_cum;
+  P.max_len = pos_map || h2o_cum ? max_len : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  trace_before("kv4_append", st);
+  kv4_append_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads), kQaThreads, 0, st>>>(P);
+  cudaError_t e = cudaGetLastError();
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_append (launch)");
+  return KVSEL_OK;
+}
+
+extern "C" kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                       const int32_t* seq_lens, int batch, const int32_t* tok_off, int total_tokens,
+                                       const int32_t* start, void* k_out, void* v_out, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  const std::string fn = "kvsel_kv4_read: ";
+  if (kvsel_status s = check_kv4(fn, kv); s != KVSEL_OK) return s;
+  if (!block_table || !seq_lens || !tok_off || batch < 1 || max_pages < 1 || total_tokens < 0)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "block_table, seq_lens, tok_off required; batch, max_pages >= 1, total_tokens >= 0");
+  if (total_tokens > 0 && (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "k_out and v_out (16-byte aligned) are required");
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < kStatusBytes)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace of at least 256 bytes is required");
+  if (total_tokens == 0) return KVSEL_OK;
+  ReadParams P;
+  fill(P, kv, block_table, max_pages, const_cast<int32_t*>(seq_lens), batch, tok_off, total_tokens, workspace);
+  P.start = start;
+  P.k = static_cast<uint4*>(k_out);
+  P.v = static_cast<uint4*>(v_out);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  trace_before("kv4_read", st);
+  kv4_read_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads), kQaThreads, 0, st>>>(P);
+  cudaError_t e = cudaGetLastError();
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_read (launch)");
+  return KVSEL_OK;
+}
+
+extern "C" size_t kvsel_kv4_evict_workspace(const kvsel_paged_kv4* kv, int batch, int budget) {
+  if (!kv || batch < 1 || budget < 1 || kv->num_kv_heads < 1) return 0;
+  return evict4_layout(batch, kv->num_kv_heads, budget).total;
+}
+
+extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* block_table, int max_pages, int32_t* seq_lens,
+                                        int batch, float* h2o_cum, int32_t* pos_map, int max_len, int budget, int n_sink,
+                                        int window, int compact, int32_t* keep_out, int32_t* freed_pages,
+                                        void* workspace, size_t ws_bytes, void* stream) {
+  const std::string fn = "kvsel_kv4_evict: ";
+  if (kvsel_status s = check_kv4(fn, kv); s != KVSEL_OK) return s;
+  if (!block_table || !seq_lens || !h2o_cum || batch < 1 || batch > 65535 || max_pages < 1 || max_len < 1)
+    return fail(KVSEL_ERR_INVALID_ARG,
+                fn + "block_table, seq_lens, h2o_cum required; 1 <= batch <= 65535; max_pages, max_len >= 1");
+  if (budget < 1 || n_sink < 0 || window < 0 || (long long)n_sink + window > budget)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "need budget >= 1, n_sink >= 0, window >= 0, n_sink + window <= budget");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace is required");
+  const Evict4Ws L = evict4_layout(batch, kv->num_kv_heads, budget);
+  if (ws_bytes < L.total) return fail(KVSEL_ERR_INVALID_ARG, fn + "workspace too small: need " + std::to_string(L.total));
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  H2OSelectArgs A;
+  A.seq_lens = seq_lens;
+  A.cum = h2o_cum;
+  A.pos_map = pos_map;
+  A.keep_slots = reinterpret_cast<int32_t*>(ws + L.keep_off);
+  A.keep_out = keep_out;
+  A.first_move = reinterpret_cast<int32_t*>(ws + L.first_off);
+  A.link = link_layout(workspace, batch * kv->num_kv_heads);
+  A.link.key = nullptr;  // counts stay 0, so no list is read
+  A.link.pos = nullptr;
+  A.status = reinterpret_cast<int*>(ws);
+  A.batch = batch;
+  A.num_kv_heads = kv->num_kv_heads;
+  A.max_len = max_len;
+  A.budget = budget;
+  A.n_sink = n_sink;
+  A.window = window;
+  if (kvsel_status s = launch_h2o_select("kvsel_kv4_evict", A, st); s != KVSEL_OK) return s;
+  if (!compact) return KVSEL_OK;
+
+  Compact4Params C;
+  C.seq_lens = seq_lens;
+  C.block_table = block_table;
+  C.keep_slots = A.keep_slots;
+  C.first_move = A.first_move;
+  C.codes[0] = static_cast<uint8_t*>(kv->k_codes);
+  C.codes[1] = static_cast<uint8_t*>(kv->v_codes);
+  C.scales[0] = static_cast<uint8_t*>(kv->k_scales);
+  C.scales[1] = static_cast<uint8_t*>(kv->v_scales);
+  C.cum = h2o_cum;
+  C.pos_map = pos_map;
+  C.status = A.status;
+  C.Hkv = kv->num_kv_heads;
+  C.max_len = max_len;
+  C.max_pages = max_pages;
+  C.num_pages = kv->num_pages;
+  C.budget = budget;
+  C.page_lg = 4 + page_shift_of(kv->page_size);
+  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(sizeof(Compact4Smem)));
+      e != cudaSuccess)
+    return cuda_fail(e, "kvsel_kv4_evict (attribute)");
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(kv->num_kv_heads) * kQcCluster, batch);
+  cfg.blockDim = dim3(kQcThreads);
+  cfg.dynamicSmemBytes = sizeof(Compact4Smem);
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kQcCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  trace_before("kv4_compact", st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_compact_kernel, C);
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (compact launch)");
+
+  H2OTruncateArgs T;
+  T.seq_lens = seq_lens;
+  T.block_table = block_table;
+  T.freed = freed_pages;
+  T.batch = batch;
+  T.max_pages = max_pages;
+  T.budget = budget;
+  T.max_len = max_len;
+  T.page_shift = page_shift_of(kv->page_size);
+  return launch_h2o_truncate("kvsel_kv4_evict", T, st);
+}

@@ -1,0 +1,857 @@
+// Decode attention over the paged 4-bit cache, with capped, biased and
+// windowed scores, per-key probabilities and the H2O cumulative score (sm_103a).
+//
+// The mathematics.  A cached key is k = s n + z per group of 32 values (codes
+// n in 0..15, kv4.cuh), so with the group's part of q
+//   q . k = sum over groups of  s (q . n) + z (sum of q)
+// and only q . n is a matrix product: the codes go to the tensor cores as they
+// are, the scale and the minimum meet the fp32 result, and no key is ever
+// dequantised.  For the values, out = sum_t p_t (s_t n_t + z_t): p_t s_t takes
+// the place of p_t in the product with the codes, and sum_t p_t z_t is one
+// number per group and head.
+//   A nibble is an fp16 number without any conversion: masked into the low
+// bits of a 16-bit half it is the subnormal n 2^-24 (or n 2^-20 four bits
+// higher), exact in the tensor cores.  Two masks give four such halves of a
+// 32-bit word, one shift the other four: 5 operations for 8 values.  The
+// powers of two go into q (or into the output).
+//   q is scaled per head by a power of two so that its largest magnitude is in
+// [2^14, 2^15): bf16 has 8 bits of mantissa, so fp16 then holds it exactly but
+// for values 2^-38 of the largest.  p s is scaled per group by a power of two
+// taken from the largest s seen so far (14 bits of headroom above fp16's
+// subnormals) and rounded to fp16: 2^-11 of its value at most, the step's only
+// rounding to 16 bits; the running maximum, the sums, the scores and the
+// output accumulate in fp32.
+//
+// main kernel: one wave of warps; each takes an equal contiguous share of
+//   the tiles of 32 tokens of all (sequence, kv head) pairs, and streams them
+//   through a private shared-memory ring with cp.async (no barrier between
+//   warps).  Rows are XOR-swizzled in 16-byte chunks, so that ldmatrix (keys)
+//   and its transposing form (values: the halves of neighbouring tokens side
+//   by side) are free of bank conflicts.  q is the left operand (heads x
+//   dims), so scores land with heads in rows, which is the layout the second
+//   product wants p in: probabilities never leave registers.  mma.sync, not
+//   tcgen05: with at most 16 rows of q the product is a sixth of what the
+//   warp-level instruction can do, and the codes reach it from registers.
+//   A warp whose share ends inside a pair leaves its m, l and partial output.
+// finalize kernel: joins the partials of each pair (one CTA per q head), turns
+//   the stored scores into probabilities and adds them up over the group's
+//   heads (one CTA per 1024 slots).
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kv4.cuh"
+
+namespace kvsel {
+
+constexpr int kQdWarps = 8;                 // warps of a CTA
+constexpr int kQdThreads = kQdWarps * 32;
+constexpr int kQdTile = 32;                 // tokens of a tile
+constexpr int kQdMaxBatch = 1024;
+constexpr int kQfSlots = 1024;              // finalize: slots per CTA
+constexpr int kQfThreads = 256;
+
+struct __align__(16) QdStage {
+  uint8_t k[kQdTile * kQ4CodeBytes];        // chunk c of row r at (c ^ ((r >> 1) & 3))
+  uint8_t v[kQdTile * kQ4CodeBytes];
+  uint4 ks[kQdTile];                        // {s, z} x 4 of row r
+  uint4 vs[kQdTile];
+  int32_t pos[kQdTile];
+};
+
+struct Decode4Params {
+  uint8_t* codes[2];
+  uint8_t* scales[2];
+  const int32_t* block_table;
+  int32_t* seq_lens;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* new_kv[2];  // appended rows, or null
+  int32_t* pos_map;
+  int32_t* next_pos;
+  const float* slopes;
+  void* out;
+  float* logits;        // [B][Hq][max_len] scores in log2 units, or null
+  float* probs;         // = logits or null
+  float* cum;
+  // workspace
+  int* status;
+  int32_t* eff_len;     // [B] length after the append, -1: rejected
+  float2* part_ml;      // [warps + pairs][G]
+  float* part_o;        // [warps + pairs][G][128]
+  float scale, softcap;
+  int window, n_sink;
+  int B, Hq, Hkv, G, max_len, max_pages, num_pages, page_lg, out_bf16, warps;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh to about 1e-7 absolute: the series where it converges fast, else from exp.
+__device__ __forceinline__ float tanh_acc(float x) {
+  const float x2 = x * x;
+  const float small = x * fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+  const float e = ex2(2.f * kLog2e * fabsf(x));
+  const float big = copysignf(1.f - __fdividef(2.f, e + 1.f), x);
+  return fabsf(x) < 0.25f ? small : big;   // e infinite: 2 / inf = 0
+}
+
+// D += A (16x16, row) * B (16x8, col), fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Tiles of a sequence that hold a key its query may see, in order: the sink
+// tiles, then those of the window (all of them without a window, or where
+// positions come from a map).
+struct TileSet {
+  int sink_tiles, win_tile, count;
+  __device__ __forceinline__ int slot0(int i) const {
+    return (i < sink_tiles ? i : win_tile + (i - sink_tiles)) * kQdTile;
+  }
+  __device__ __forceinline__ bool holds(int tile) const { return tile < sink_tiles || tile >= win_tile; }
+};
+__device__ __forceinline__ TileSet tiles_of(int S, int window, int n_sink, bool mapped) {
+  const int nt = (S + kQdTile - 1) / kQdTile;
+  TileSet t{0, 0, nt};
+  if (window > 0 && !mapped && S > window) {
+    const int w0 = (S - window) / kQdTile, a = (min(n_sink, S) + kQdTile - 1) / kQdTile;
+    if (a < w0) t = TileSet{a, w0, a + nt - w0};
+  }
+  return t;
+}
+
+// Length of sequence b after the append, or -1 if it does not fit.
+__device__ __forceinline__ int checked_len(const Decode4Params& P, int b) {
+  const int s0 = __ldcg(P.seq_lens + b), add = P.new_kv[0] ? 1 : 0;
+  const long long cap = min((long long)P.max_len, (long long)P.max_pages << P.page_lg);
+  return s0 < 0 || (long long)s0 + add > cap ? -1 : s0 + add;
+}
+
+// kWide: more than 8 q heads a kv head (two blocks of 8 rows).  kMod: scores
+// are capped, biased or windowed, or positions come from a map.
+template <bool kWide, bool kMod, int kStages>
+__global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(const Decode4Params P) {
+  constexpr int kH = kWide ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t qd_smem[];
+  __shared__ int s_tiles[kQdMaxBatch + 1];   // exclusive prefix of the sequences' tile counts
+  __shared__ int s_scan[kQdWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const bool mapped = P.pos_map != nullptr;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the share of this warp
+  int carry = 0;
+  for (int b0 = 0; b0 < P.B; b0 += kQdThreads) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < P.B) {
+      const int S = checked_len(P, b);
+      if (blockIdx.x == 0) {
+        P.eff_len[b] = S;
+        if (S < 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+      }
+      n = S > 0 ? tiles_of(S, P.window, P.n_sink, mapped).count : 0;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int base = carry, sum = carry;
+#pragma unroll
+    for (int w = 0; w < kQdWarps; ++w) {
+      if (w < warp) base += s_scan[w];
+      sum += s_scan[w];
+    }
+    if (b < P.B) s_tiles[b] = base + x - n;
+    carry = sum;
+    __syncthreads();
+  }
+  if (tid == 0) s_tiles[P.B] = carry;
+  __syncthreads();
+  const long long T = (long long)carry * P.Hkv;
+  const long long N = min((long long)P.warps, T);
+  const long long wid = (long long)blockIdx.x * kQdWarps + warp;
+  if (wid >= N) return;
+  long long tile = wid * T / N;
+  const long long tile_end = (wid + 1) * T / N;
+
+  QdStage* ring = reinterpret_cast<QdStage*>(qd_smem) + warp * kStages;
+  const int page_mask = (1 << P.page_lg) - 1;
+
+  // ---- one (sequence, kv head) pair after the other
+#pragma unroll 1
+  while (tile < tile_end) {
+    int b;
+    {
+      int lo = 0, hi = P.B - 1;   // last b with Hkv * s_tiles[b] <= tile
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)s_tiles[mid] * P.Hkv <= tile) lo = mid;
+        else hi = mid - 1;
+      }
+      b = lo;
+    }
+    const int nb = s_tiles[b + 1] - s_tiles[b];
+    const long long in_b = tile - (long long)s_tiles[b] * P.Hkv;
+    const int kvh = int(in_b / nb), i0 = int(in_b - (long long)kvh * nb);
+    const int i1 = int(min((long long)nb, i0 + (tile_end - tile)));
+    const int S = checked_len(P, b);
+    const TileSet ts = tiles_of(S, P.window, P.n_sink, mapped);
+    const int32_t* bt = P.block_table + (size_t)b * P.max_pages;
+    const size_t rowi = (size_t)b * P.Hkv + kvh;
+    int32_t* prow = mapped ? P.pos_map + rowi * P.max_len : nullptr;
+    const bool append = P.new_kv[0] != nullptr;
+    int pos_q = S - 1;
+    if (kMod && mapped) pos_q = append ? __ldcg(P.next_pos + b) : __ldcg(prow + S - 1);
+
+    // q of this thread's head rows: fragments, group sums, power-of-two scale
+    uint32_t qa[kH][4][4];   // per group: {dims 0,4}, {1,5}/16, {2,6}, {3,7}/16 of the thread's word
+    float qs[kH][4], mult[kH], slope[kH];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      const int head = g8 + 8 * h;
+      uint4 raw[4];
+      uint32_t top = 0;
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        raw[gq] = make_uint4(0, 0, 0, 0);
+        if (head < P.G)
+          raw[gq] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)b * P.Hq + kvh * P.G + head) * kQ4D + 32 * gq + 8 * t4));
+        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max((r[i] << 16) & 0x7F800000u, r[i] & 0x7F800000u));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest magnitude in [2^(e-127), 2^(e-126)), e = top >> 23; q' = q 2^(14-(e-127))
+      const int e = max(int(top >> 23), 15);
+      const float up = __uint_as_float(uint32_t(268 - e) << 23);   // 13 <= 268 - e <= 253
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
+        float x[8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = bf16lo_to_f32(r[i]) * up;
+          x[2 * i + 1] = bf16hi_to_f32(r[i]) * up;
+          sum += x[2 * i] + x[2 * i + 1];
+        }
+        qa[h][gq][0] = pack_f16x2(x[0], x[4]);
+        qa[h][gq][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
+        qa[h][gq][2] = pack_f16x2(x[2], x[6]);
+        qa[h][gq][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        qs[h][gq] = sum * 0x1p-24f;   // as if it had come out of the product with the codes
+      }
+      // a product with the codes is 2^(141-e-24) times the true one
+      mult[h] = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
+      slope[h] = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
+      if (!kMod) mult[h] *= kLog2e;
+    }
+
+    float m[kH], l[kH], zacc[kH][4], o[kH][4][8];
+    int e_v[4];               // per group: 2^e_v is above every value scale so far
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        zacc[h][gq] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[h][gq][i] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int gq = 0; gq < 4; ++gq) e_v[gq] = 28;   // scales are 0 or at least 2^-100
+
+    // copies of tile i into its stage; bad pages and slots past S leave zeros
+    auto fetch = [&](int i) {
+      QdStage& st = ring[(i - i0) % kStages];
+      const int s0 = ts.slot0(i);
+      const int r0 = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int s1 = s0 + 16 * half;
+        int phys = -1;
+        if (s1 < S) phys = __ldg(bt + (s1 >> P.page_lg));
+        const bool ok = unsigned(phys) < unsigned(P.num_pages);
+        const long long base = ((((long long)(ok ? phys : 0) * P.Hkv + kvh)) << P.page_lg) + (s1 & page_mask);
+        const int bytes = ok ? 16 : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = 8 * k + r0, row = 16 * half + r;
+          const int off = row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4);
+          const size_t src = (size_t)(base + r) * kQ4CodeBytes + c * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st.k + off)), "l"(P.codes[0] + src), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st.v + off)), "l"(P.codes[1] + src), "r"(bytes) : "memory");
+        }
+        const int r = lane & 15, side = lane >> 4;
+        const size_t src = (size_t)(base + r) * kQ4ScaleBytes;
+        uint4* dst = (side ? st.vs : st.ks) + 16 * half + r;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(P.scales[side] + src), "r"(bytes) : "memory");
+      }
+      if (kMod && mapped) {
+        const int s = s0 + lane;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(st.pos + lane)), "l"(prow + min(s, S - 1)), "r"(s < S ? 4 : 0) : "memory");
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+      if (i0 + k < i1) fetch(i0 + k);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();
+      // the stage read last is free now: the next tile goes there
+      if (i + kStages - 1 < i1) fetch(i + kStages - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      QdStage& st = ring[(i - i0) % kStages];
+      const int s0 = ts.slot0(i);
+
+      // ---- the appended token: quantised here, into the pool and into this tile
+      if (append && s0 <= S - 1 && S - 1 < s0 + kQdTile) {
+        const int row = S - 1 - s0;
+        const int phys = __ldg(bt + ((S - 1) >> P.page_lg));
+        if (unsigned(phys) < unsigned(P.num_pages)) {
+          const long long prow_i = ((((long long)phys * P.Hkv + kvh)) << P.page_lg) + ((S - 1) & page_mask);
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(P.new_kv[side] + rowi * kQ4D) + lane);
+            const uint32_t raw[2] = {x.x, x.y};
+            uint32_t sz;
+            const uint32_t codes = q4_group<4>(raw, sz);
+            reinterpret_cast<uint16_t*>(P.codes[side] + prow_i * kQ4CodeBytes)[lane] = uint16_t(codes);
+            const int off = row * kQ4CodeBytes + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2;
+            *reinterpret_cast<uint16_t*>((side ? st.v : st.k) + off) = uint16_t(codes);
+            if ((lane & 7) == 0) {
+              reinterpret_cast<uint32_t*>(P.scales[side] + prow_i * kQ4ScaleBytes)[lane >> 3] = sz;
+              reinterpret_cast<uint32_t*>((side ? st.vs : st.ks) + row)[lane >> 3] = sz;
+            }
+          }
+        }
+        if (mapped && lane == 0) {
+          const int np = __ldcg(P.next_pos + b);
+          prow[S - 1] = np;
+          st.pos[row] = np;
+        }
+        __syncwarp();
+      }
+
+      // ---- which of the 32 keys are seen (lane t: token t)
+      uint32_t vis;
+      {
+        const int s = s0 + lane;
+        bool see = s < S;
+        if (see) see = unsigned(__ldg(bt + (s >> P.page_lg))) < unsigned(P.num_pages);
+        if (s < S && !see) report(P.status, KVSEL_ERR_BAD_INDEX);
+        if (kMod && P.window > 0) {
+          const int p = mapped ? st.pos[lane] : s;
+          see = see && (pos_q - p < P.window || p < P.n_sink);
+        }
+        vis = __ballot_sync(0xffffffffu, see);
+        // what is not seen must not reach the product with p = 0 as NaN or infinity
+        uint4 own = st.vs[lane];
+        if (!see) {
+          own = make_uint4(0, 0, 0, 0);
+          st.vs[lane] = own;
+        }
+        // the scales' running exponents
+        const uint32_t sc[4] = {own.x & 0x7F80u, own.y & 0x7F80u, own.z & 0x7F80u, own.w & 0x7F80u};
+        bool grow = false;
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) grow |= int(sc[gq] >> 7) >= e_v[gq];
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int gq = 0; gq < 4; ++gq) {
+            // exponent field + 1: s < 2^(field + 1 - 127); a NaN's field counts as the largest finite one
+            const int e = min(int(__reduce_max_sync(0xffffffffu, sc[gq])) >> 7, 253) + 1;
+            if (e > e_v[gq]) {
+              const float down = __uint_as_float(uint32_t(max(0, 127 - (e - e_v[gq]))) << 23);
+#pragma unroll
+              for (int h = 0; h < kH; ++h)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[h][gq][k] *= down;
+              e_v[gq] = e;
+            }
+          }
+        }
+        __syncwarp();
+      }
+
+      // ---- scores: heads g8 (+ 8) x tokens 8 j + 2 t4, + 1
+      float x[kH][4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // words t4 of groups 0..3 of token 8 j + g8: matrix i of the load is group i
+        uint32_t w[4];
+        {
+          const int row = 8 * j + (lane & 7), c = lane >> 3;
+          ldsm_x4(smem_u32(st.k + row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4)), w[0], w[1], w[2], w[3]);
+        }
+        const uint4 sz0 = st.ks[8 * j + 2 * t4], sz1 = st.ks[8 * j + 2 * t4 + 1];
+        const uint32_t a0[4] = {sz0.x, sz0.y, sz0.z, sz0.w}, a1[4] = {sz1.x, sz1.y, sz1.z, sz1.w};
+#pragma unroll
+        for (int h = 0; h < kH; ++h) x[h][j][0] = x[h][j][1] = 0.f;
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          const uint32_t hi = w[gq] >> 8;
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16_16816(c, qa[0][gq][0], kWide ? qa[kH - 1][gq][0] : 0u, qa[0][gq][1], kWide ? qa[kH - 1][gq][1] : 0u,
+                        w[gq] & 0x000F000Fu, w[gq] & 0x00F000F0u);
+          mma_f16_16816(c, qa[0][gq][2], kWide ? qa[kH - 1][gq][2] : 0u, qa[0][gq][3], kWide ? qa[kH - 1][gq][3] : 0u,
+                        hi & 0x000F000Fu, hi & 0x00F000F0u);
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            x[h][j][0] = fmaf(bf16lo_to_f32(a0[gq]), c[2 * h], fmaf(bf16hi_to_f32(a0[gq]), qs[h][gq], x[h][j][0]));
+            x[h][j][1] = fmaf(bf16lo_to_f32(a1[gq]), c[2 * h + 1], fmaf(bf16hi_to_f32(a1[gq]), qs[h][gq], x[h][j][1]));
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float y = x[h][j][k] * mult[h];
+            if (kMod) {
+              if (P.softcap > 0.f) y = P.softcap * tanh_acc(__fdividef(y, P.softcap));
+              y *= kLog2e;
+              if (P.slopes) {
+                const int t = 8 * j + 2 * t4 + k;
+                const int p = mapped ? st.pos[t] : s0 + t;
+                y = fmaf(-slope[h], fabsf(float(pos_q - p)), y);
+              }
+            }
+            x[h][j][k] = (vis >> (8 * j + 2 * t4 + k)) & 1u ? y : -INFINITY;
+          }
+        if (P.logits && g8 + 8 * h < P.G) {
+          float* lrow = P.logits + ((size_t)b * P.Hq + kvh * P.G + g8 + 8 * h) * P.max_len + s0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = 8 * j + 2 * t4 + k;
+              if (s0 + t < S) lrow[t] = x[h][j][k];
+            }
+        }
+        // running maximum and sum
+        float mx = m[h];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[h][j][0], x[h][j][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float use = mx == -INFINITY ? 0.f : mx;
+        if (__any_sync(0xffffffffu, mx > m[h])) {
+          const float corr = ex2(m[h] - use);
+          m[h] = mx;
+          l[h] *= corr;
+#pragma unroll
+          for (int gq = 0; gq < 4; ++gq) zacc[h][gq] *= corr;
+          // the output has heads in its columns 2 t4, 2 t4 + 1
+          const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4), c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
+#pragma unroll
+          for (int gq = 0; gq < 4; ++gq)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[h][gq][k] *= (k & 1) ? c1 : c0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            x[h][j][k] = ex2(x[h][j][k] - use);
+            l[h] += x[h][j][k];
+          }
+      }
+
+      // ---- output: (dims x tokens) codes times (tokens x heads) p s, per group
+      float inv_e[4];
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) inv_e[gq] = __uint_as_float(uint32_t(268 - e_v[gq]) << 23);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pb[kH][4][2];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * half + jj;
+          const uint4 sz0 = st.vs[8 * j + 2 * t4], sz1 = st.vs[8 * j + 2 * t4 + 1];
+          const uint32_t a0[4] = {sz0.x, sz0.y, sz0.z, sz0.w}, a1[4] = {sz1.x, sz1.y, sz1.z, sz1.w};
+#pragma unroll
+          for (int gq = 0; gq < 4; ++gq) {
+            const float f0 = bf16lo_to_f32(a0[gq]) * inv_e[gq], f1 = bf16lo_to_f32(a1[gq]) * inv_e[gq];
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+              pb[h][gq][jj] = pack_f16x2(x[h][j][0] * f0, x[h][j][1] * f1);
+              zacc[h][gq] = fmaf(x[h][j][0], bf16hi_to_f32(a0[gq]), fmaf(x[h][j][1], bf16hi_to_f32(a1[gq]), zacc[h][gq]));
+            }
+          }
+        }
+        // halves g8 of groups 0..3, tokens 2 t4 and 2 t4 + 1 of the 8 (lo) and the next 8 (hi)
+        uint32_t lo[4], hi[4];
+        {
+          const int row = 16 * half + (lane & 7), c = lane >> 3;
+          const int off = ((c ^ ((row >> 1) & 3)) << 4);
+          ldsm_x4_t(smem_u32(st.v + row * kQ4CodeBytes + off), lo[0], lo[1], lo[2], lo[3]);
+          ldsm_x4_t(smem_u32(st.v + (row + 8) * kQ4CodeBytes + off), hi[0], hi[1], hi[2], hi[3]);
+        }
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          const uint32_t l8 = lo[gq] >> 8, h8 = hi[gq] >> 8;
+          const uint32_t a[8] = {lo[gq] & 0x000F000Fu, lo[gq] & 0x00F000F0u, hi[gq] & 0x000F000Fu, hi[gq] & 0x00F000F0u,
+                                 l8 & 0x000F000Fu,     l8 & 0x00F000F0u,     h8 & 0x000F000Fu,     h8 & 0x00F000F0u};
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            float(&o0)[4] = *reinterpret_cast<float(*)[4]>(&o[h][gq][0]);
+            float(&o1)[4] = *reinterpret_cast<float(*)[4]>(&o[h][gq][4]);
+            mma_f16_16816(o0, a[0], a[1], a[2], a[3], pb[h][gq][0], pb[h][gq][1]);
+            mma_f16_16816(o1, a[4], a[5], a[6], a[7], pb[h][gq][0], pb[h][gq][1]);
+          }
+        }
+      }
+      __syncwarp();   // this stage may be overwritten
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+
+    // ---- the partial result: dims 32 g + 4 g8 + {0..3} of heads 2 t4, 2 t4 + 1
+    const long long slot = wid + rowi;   // the staircase of (warp, pair) visits each sum once
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      float lsum = l[h];
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+      if (t4 == 0 && g8 + 8 * h < P.G) P.part_ml[slot * P.G + g8 + 8 * h] = make_float2(m[h], lsum);
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        float z = zacc[h][gq];
+        z += __shfl_xor_sync(0xffffffffu, z, 1);
+        z += __shfl_xor_sync(0xffffffffu, z, 2);
+        const float z0 = __shfl_sync(0xffffffffu, z, 8 * t4), z1 = __shfl_sync(0xffffffffu, z, 8 * t4 + 4);
+        // codes were n 2^-24 (dims 0, 2) and n 2^-20 (dims 1, 3), p s was p s 2^(141 - e): undone in
+        // two factors so that neither overflows
+        const float back = __uint_as_float(uint32_t(e_v[gq] - 14) << 23);
+        const float* a = o[h][gq];
+        const float c24 = 0x1p24f, c20 = 0x1p20f;
+        const float4 r0 = make_float4(fmaf(a[0] * c24, back, z0), fmaf(a[2] * c20, back, z0),
+                                      fmaf(a[4] * c24, back, z0), fmaf(a[6] * c20, back, z0));
+        const float4 r1 = make_float4(fmaf(a[1] * c24, back, z1), fmaf(a[3] * c20, back, z1),
+                                      fmaf(a[5] * c24, back, z1), fmaf(a[7] * c20, back, z1));
+        const int head = 8 * h + 2 * t4;
+        float* po = P.part_o + (slot * P.G + head) * kQ4D + 32 * gq + 4 * g8;
+        if (head < P.G) *reinterpret_cast<float4*>(po) = r0;
+        if (head + 1 < P.G) *reinterpret_cast<float4*>(po + kQ4D) = r1;
+      }
+    }
+    tile += i1 - i0;
+  }
+}
+
+// Joins a pair's partials.  blockIdx.x < G: the output of one q head; beyond:
+// probabilities and cumulative scores of 1024 slots.
+__global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4Params P) {
+  __shared__ float s_m[16], s_inv[16];
+  __shared__ float s_red[kQfThreads / 32];
+  __shared__ float s_o[kQfThreads / 32][kQ4D];
+  __shared__ int s_pre[kQfThreads / 32], s_tot[kQfThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kvh = blockIdx.y, b = blockIdx.z;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool mapped = P.pos_map != nullptr;
+  const int S = __ldcg(P.eff_len + b);
+  if (S < 0) return;
+  const int chunk = int(blockIdx.x) - P.G;
+  if (chunk < 0 && blockIdx.x == 0 && kvh == 0 && tid == 0 && P.new_kv[0]) {
+    P.seq_lens[b] = S;   // the main kernel is done with the lengths, and this one reads eff_len
+    if (P.next_pos) P.next_pos[b] += 1;
+  }
+  if (chunk >= 0 && chunk * kQfSlots >= S) return;
+
+  // tiles before this sequence, and of all
+  int pre = 0, tot = 0;
+  for (int i = tid; i < P.B; i += kQfThreads) {
+    const int Si = __ldcg(P.eff_len + i);
+    const int n = Si > 0 ? tiles_of(Si, P.window, P.n_sink, mapped).count : 0;
+    tot += n;
+    if (i < b) pre += n;
+  }
+  pre = __reduce_add_sync(0xffffffffu, pre);
+  tot = __reduce_add_sync(0xffffffffu, tot);
+  if (lane == 0) {
+    s_pre[warp] = pre;
+    s_tot[warp] = tot;
+  }
+  __syncthreads();
+  pre = tot = 0;
+#pragma unroll
+  for (int w = 0; w < kQfThreads / 32; ++w) {
+    pre += s_pre[w];
+    tot += s_tot[w];
+  }
+  const TileSet ts = tiles_of(S, P.window, P.n_sink, mapped);
+  const long long T = (long long)tot * P.Hkv, N = min((long long)P.warps, T);
+  const long long t0 = (long long)pre * P.Hkv + (long long)kvh * ts.count;
+  const size_t rowi = (size_t)b * P.Hkv + kvh;
+  int w0 = 0, n_part = 0;
+  if (ts.count > 0) {   // warp w owns tiles [w T / N, (w + 1) T / N)
+    w0 = int(((t0 + 1) * N - 1) / T);
+    n_part = int(((t0 + ts.count) * N - 1) / T) - w0 + 1;
+  }
+  const long long first = (long long)w0 + (long long)rowi;
+
+  if (chunk < 0) {
+    const int head = blockIdx.x;
+    float mx = -INFINITY;
+    for (int i = tid; i < n_part; i += kQfThreads) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) s_red[warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQfThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
+    const float use = mx == -INFINITY ? 0.f : mx;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lsum = 0.f;
+    for (int i = warp; i < n_part; i += kQfThreads / 32) {
+      const float2 ml = __ldcg(&P.part_ml[(first + i) * P.G + head]);
+      const float f = ex2(ml.x - use);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(P.part_o + ((first + i) * P.G + head) * kQ4D) + lane);
+      lsum = fmaf(ml.y, f, lsum);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+    __syncthreads();
+    if (lane == 0) s_red[warp] = lsum;
+    __syncthreads();
+    if (tid < kQ4D) {
+      float sum = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kQfThreads / 32; ++w) {
+        sum += s_red[w];
+        v += s_o[w][tid];
+      }
+      v = sum == 0.f ? 0.f : v / sum;   // nothing seen: 0
+      const size_t at = ((size_t)b * P.Hq + kvh * P.G + head) * kQ4D + tid;
+      if (P.out_bf16) static_cast<__nv_bfloat16*>(P.out)[at] = __float2bfloat16(v);
+      else static_cast<float*>(P.out)[at] = v;
+    }
+    return;
+  }
+
+  // every head's maximum and 1 / sum: 16 threads a head
+  {
+    const int head = tid >> 4, l16 = tid & 15;
+    float mx = -INFINITY;
+    if (head < P.G)
+      for (int i = l16; i < n_part; i += 16) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float use = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    if (head < P.G)
+      for (int i = l16; i < n_part; i += 16) {
+        const float2 ml = __ldcg(&P.part_ml[(first + i) * P.G + head]);
+        sum = fmaf(ml.y, ex2(ml.x - use), sum);
+      }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (l16 == 0) {
+      s_m[head] = use;
+      s_inv[head] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+  }
+  __syncthreads();
+  const float* lg = P.logits + ((size_t)b * P.Hq + kvh * P.G) * P.max_len;
+  float* crow = P.cum ? P.cum + rowi * P.max_len : nullptr;
+  const int new_slot = P.new_kv[0] ? S - 1 : -1;
+#pragma unroll
+  for (int k = 0; k < kQfSlots / kQfThreads; ++k) {
+    const int s = chunk * kQfSlots + k * kQfThreads + tid;
+    if (s >= S) break;
+    const bool visited = ts.holds(s / kQdTile);
+    float sum = 0.f;
+#pragma unroll 8
+    for (int h = 0; h < P.G; ++h) {
+      const float p = visited ? ex2(__ldcg(lg + (size_t)h * P.max_len + s) - s_m[h]) * s_inv[h] : 0.f;
+      if (P.probs) P.probs[((size_t)b * P.Hq + kvh * P.G + h) * P.max_len + s] = p;
+      sum += p;
+    }
+    if (crow && (visited || s == new_slot)) crow[s] = s == new_slot ? sum : crow[s] + sum;
+  }
+}
+
+}  // namespace kvsel
+
+using namespace kvsel;
+using namespace kvsel_host;
+
+namespace {
+
+constexpr int kQdStages = 2;
+
+struct Decode4Ws {
+  size_t eff_off, ml_off, o_off, logits_off, total;
+};
+
+// CTAs of the main kernel: every co-resident slot (8 warps each; two CTAs an
+// SM up to 8 q heads a kv head, one above).
+int decode4_ctas(int G) { return sm_count() * (G > 8 ? 1 : 2); }
+
+// The workspace is sized for the largest grid the device could take; the
+// number of SMs is that of the current device.
+Decode4Ws decode4_layout(const kvsel_paged_kv4* kv, int batch, int max_len, bool own_logits, int ctas) {
+  const int G = kv->num_q_heads / kv->num_kv_heads;
+  const size_t parts = size_t(ctas) * kQdWarps + size_t(batch) * kv->num_kv_heads;
+  Decode4Ws w;
+  w.eff_off = kStatusBytes;
+  w.ml_off = align_up(w.eff_off + size_t(batch) * 4, 256);
+  w.o_off = align_up(w.ml_off + parts * G * sizeof(float2), 256);
+  w.logits_off = align_up(w.o_off + parts * G * kQ4D * sizeof(float), 256);
+  w.total = w.logits_off + (own_logits ? align_up(size_t(batch) * kv->num_q_heads * max_len * sizeof(float), 256) : 0);
+  return w;
+}
+
+kvsel_status check_shape(const std::string& fn, const kvsel_paged_kv4* kv) {
+  if (!kv || kv->num_kv_heads < 1 || kv->num_pages < 1 || kv->num_q_heads < 1 || kv->num_q_heads % kv->num_kv_heads != 0)
+    return fail(KVSEL_ERR_INVALID_ARG,
+                fn + "a cache descriptor with num_pages, num_kv_heads >= 1 and num_q_heads a multiple of num_kv_heads is required");
+  if (page_shift_of(kv->page_size) < 0 || kv->head_dim != kQ4D)
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "only head_dim 128 and page_size 16, 32, 64, 128 or 256 are implemented");
+  if (kv->num_q_heads / kv->num_kv_heads > 16)
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "at most 16 q heads per kv head are implemented");
+  return KVSEL_OK;
+}
+
+template <bool kWide, bool kMod>
+kvsel_status launch_main(const Decode4Params& P, int ctas, cudaStream_t st) {
+  auto* fn = &kv4_decode_kernel<kWide, kMod, kQdStages>;
+  const int smem = int(sizeof(QdStage)) * kQdStages * kQdWarps;
+  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(fn), smem); e != cudaSuccess)
+    return cuda_fail(e, "kvsel_kv4_decode_attn (attribute)");
+  trace_before("kv4_decode", st);
+  fn<<<ctas, kQdThreads, smem, st>>>(P);
+  cudaError_t e = cudaGetLastError();
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_decode_attn (launch)");
+  return KVSEL_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kvsel_kv4_decode_attn_workspace(const kvsel_paged_kv4* kv, int batch, int max_len, int with_probs,
+                                                  int with_cum) {
+  if (batch < 1 || batch > kQdMaxBatch || max_len < 1 || check_shape("", kv) != KVSEL_OK) return 0;
+  return decode4_layout(kv, batch, max_len, with_cum && !with_probs, decode4_ctas(kv->num_q_heads / kv->num_kv_heads)).total;
+}
+
+extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                              int32_t* seq_lens, int batch, const void* q, const void* k_new,
+                                              const void* v_new, int32_t* pos_map, int32_t* next_pos, float scale,
+                                              const kvsel_score_mod* mod, void* out, int out_dtype, float* probs,
+                                              float* h2o_cum, int max_len, void* workspace, size_t ws_bytes,
+                                              void* stream) {
+  const std::string fn = "kvsel_kv4_decode_attn: ";
+  if (kvsel_status s = check_shape(fn, kv); s != KVSEL_OK) return s;
+  for (const void* p : {kv->k_codes, kv->v_codes, kv->k_scales, kv->v_scales})
+    if (!p || !aligned(p, 16)) return fail(KVSEL_ERR_INVALID_ARG, fn + "k_codes, v_codes, k_scales and v_scales (16-byte aligned) are required");
+  if (!block_table || !seq_lens || !q || !out || max_pages < 1 || max_len < 1)
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "block_table, seq_lens, q, out required; max_pages, max_len >= 1");
+  if (batch < 1 || batch > kQdMaxBatch) return fail(KVSEL_ERR_INVALID_ARG, fn + "1 <= batch <= 1024");
+  if (kv->num_kv_heads > 65535) return fail(KVSEL_ERR_UNSUPPORTED, fn + "at most 65535 kv heads");
+  if ((k_new == nullptr) != (v_new == nullptr)) return fail(KVSEL_ERR_INVALID_ARG, fn + "k_new and v_new go together");
+  if (pos_map && k_new && !next_pos) return fail(KVSEL_ERR_INVALID_ARG, fn + "pos_map needs next_pos when a token is appended");
+  if (out_dtype != KVSEL_BF16 && out_dtype != KVSEL_F32) return fail(KVSEL_ERR_INVALID_ARG, fn + "out_dtype must be KVSEL_BF16 or KVSEL_F32");
+  if (!aligned(q, 16) || (k_new && (!aligned(k_new, 16) || !aligned(v_new, 16))))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "q, k_new and v_new must be 16-byte aligned");
+  // the comparisons refuse NaN too
+  if (mod && (!(mod->softcap >= 0.f) || mod->softcap > 1e30f || mod->window < 0 || mod->n_sink < 0))
+    return fail(KVSEL_ERR_INVALID_ARG, fn + "need 0 <= softcap <= 1e30, window >= 0, n_sink >= 0");
+  if (!workspace || !aligned(workspace, 256)) return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace is required");
+  const int G = kv->num_q_heads / kv->num_kv_heads;
+  const int ctas = decode4_ctas(G);
+  const bool own_logits = h2o_cum && !probs;
+  const Decode4Ws L = decode4_layout(kv, batch, max_len, own_logits, ctas);
+  if (ws_bytes < L.total) return fail(KVSEL_ERR_INVALID_ARG, fn + "workspace too small: need " + std::to_string(L.total));
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Decode4Params P;
+  P.codes[0] = static_cast<uint8_t*>(kv->k_codes);
+  P.codes[1] = static_cast<uint8_t*>(kv->v_codes);
+  P.scales[0] = static_cast<uint8_t*>(kv->k_scales);
+  P.scales[1] = static_cast<uint8_t*>(kv->v_scales);
+  P.block_table = block_table;
+  P.seq_lens = seq_lens;
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.new_kv[0] = static_cast<const __nv_bfloat16*>(k_new);
+  P.new_kv[1] = static_cast<const __nv_bfloat16*>(v_new);
+  P.pos_map = pos_map;
+  P.next_pos = k_new ? next_pos : nullptr;
+  P.slopes = mod ? mod->slopes : nullptr;
+  P.out = out;
+  P.logits = probs ? probs : own_logits ? reinterpret_cast<float*>(ws + L.logits_off) : nullptr;
+  P.probs = probs;
+  P.cum = h2o_cum;
+  P.status = reinterpret_cast<int*>(ws);
+  P.eff_len = reinterpret_cast<int32_t*>(ws + L.eff_off);
+  P.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
+  P.part_o = reinterpret_cast<float*>(ws + L.o_off);
+  P.scale = scale;
+  P.softcap = mod ? mod->softcap : 0.f;
+  P.window = mod ? mod->window : 0;
+  P.n_sink = mod ? mod->n_sink : 0;
+  P.B = batch;
+  P.Hq = kv->num_q_heads;
+  P.Hkv = kv->num_kv_heads;
+  P.G = G;
+  P.max_len = max_len;
+  P.max_pages = max_pages;
+  P.num_pages = kv->num_pages;
+  P.page_lg = 4 + page_shift_of(kv->page_size);
+  P.out_bf16 = out_dtype == KVSEL_BF16;
+  P.warps = ctas * kQdWarps;
+  const bool modded = P.softcap > 0.f || P.slopes || P.window > 0;
+  kvsel_status s = G > 8 ? (modded ? launch_main<true, true>(P, ctas, st) : launch_main<true, false>(P, ctas, st))
+                         : (modded ? launch_main<false, true>(P, ctas, st) : launch_main<false, false>(P, ctas, st));
+  if (s != KVSEL_OK) return s;
+
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(G) + (P.logits ? unsigned((max_len + kQfSlots - 1) / kQfSlots) : 0u), kv->num_kv_heads, batch);
+  cfg.blockDim = dim3(kQfThreads);
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  trace_before("kv4_finalize", st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_finalize_kernel, P);
+  trace_after(st);
+  if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_decode_attn (finalize launch)");
+  return KVSEL_OK;
+}

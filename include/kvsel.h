@@ -663,6 +663,121 @@ KVSEL_API kvsel_status kvsel_quest_decode(const kvsel_paged_kv* kv, const int32_
                                           int32_t* pages_out, float* bounds_out, void* workspace,
                                           size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged 4-bit KV cache.
+ *
+ * A row (one token's K or V of one kv head, 128 values) is four groups of 32
+ * along the head dimension.  A group holds
+ *   z = its minimum (bf16, exact),
+ *   s = (max - min) / 15 rounded to bf16, 0 if that is below 2^-100,
+ *   n = (x - z) / s rounded to nearest, ties to even, within 0..15 (0 if s is
+ *       0), four bits each,
+ * and stands for s * n + z.  Both roundings are those of the exact quotient.
+ * A group with a NaN, an infinity or a magnitude above 2^126 is held as NaN.
+ * Layout, K and V alike:
+ *   codes   [num_pages][num_kv_heads][page_size][64] bytes: value 2i of the
+ *           row in the low half of byte i, value 2i + 1 in the high half
+ *   scales  bf16 [num_pages][num_kv_heads][page_size][4][2]: {s, z} per group
+ * 80 bytes a row instead of 256.  Pages, block table and lengths are those of
+ * the bf16 cache; head_dim 128, page_size 16, 32, 64, 128 or 256 (else
+ * KVSEL_ERR_UNSUPPORTED).  Every pool must be 16-byte aligned.
+ */
+typedef struct kvsel_paged_kv4 {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t num_q_heads; /* q head h reads kv head h / (num_q_heads/num_kv_heads) */
+  int32_t head_dim;    /* 128 */
+  int32_t page_size;   /* 16, 32, 64, 128 or 256 */
+} kvsel_paged_kv4;
+
+/* Quantise new tokens into the cache: sequence b appends the packed rows
+ * [tok_off[b], tok_off[b + 1]) behind its seq_lens[b] live ones.
+ *   block_table  int32 [batch][max_pages]; the pages of the new slots are in it.
+ *   seq_lens     int32 [batch], in/out: grows by each sequence's run.
+ *   tok_off      int32 [batch + 1] (device), non-decreasing from 0 on, at most
+ *                total_tokens; packed rows past tok_off[batch] are ignored.
+ *   k, v         bf16 [total_tokens][num_kv_heads][128].
+ *   pos_map      int32 [batch][num_kv_heads][max_len] or NULL: the new slots get
+ *                next_pos[b], next_pos[b] + 1, ...
+ *   next_pos     int32 [batch] or NULL (required with pos_map): grows with seq_lens.
+ *   h2o_cum      fp32 [batch][num_kv_heads][max_len] or NULL: new slots start at 0.
+ *   workspace    >= kvsel_kv4_append_workspace() bytes, zeroed before first use;
+ *                calls that may overlap on the GPU need workspaces of their own.
+ * Device-detected problems (bad offsets, a run beyond the table or max_len, a
+ * page outside the pool) record KVSEL_ERR_BAD_INDEX; a sequence whose run does
+ * not fit is left as it was.  One launch. */
+KVSEL_API size_t kvsel_kv4_append_workspace(const kvsel_paged_kv4* kv, int batch);
+KVSEL_API kvsel_status kvsel_kv4_append(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                        int32_t* seq_lens, int batch, const int32_t* tok_off, int total_tokens,
+                                        const void* k, const void* v, int32_t* pos_map, int32_t* next_pos,
+                                        float* h2o_cum, int max_len, void* workspace, size_t ws_bytes, void* stream);
+
+/* Read cached tokens back as bf16 (s * n + z in fp32, rounded once): packed row
+ * tok_off[b] + i <- slot start[b] + i of sequence b.
+ *   seq_lens     int32 [batch], read only: slots at or past it are not read.
+ *   start        int32 [batch] or NULL (from slot 0).
+ *   k_out, v_out bf16 [total_tokens][num_kv_heads][128]; rows past tok_off[batch]
+ *                and rows with a problem (KVSEL_ERR_BAD_INDEX) stay as they are.
+ *   workspace    >= 256 bytes: the status word.  One launch. */
+KVSEL_API kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                      const int32_t* seq_lens, int batch, const int32_t* tok_off, int total_tokens,
+                                      const int32_t* start, void* k_out, void* v_out, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* Decode step over the 4-bit cache: append (optional), attention, each key's
+ * probability, the H2O cumulative score.  With S_b the live length after the
+ * append, for q head h of kv head g (every k, v as the cache stands for them):
+ *   t_j = scale * q_h . k_j
+ *   t_j = softcap * tanh(t_j / softcap)             if mod->softcap > 0
+ *   t_j = t_j - slopes[h] * |pos_q - pos_j|         if mod->slopes
+ *   key j is seen if j < S_b and, with mod->window > 0, pos_q - pos_j < window
+ *   or pos_j < n_sink
+ *   p_j = softmax over the seen keys (0 for the others), out_h = sum p_j v_j,
+ *   cum[b][g][j] += sum over the group's heads of p_j
+ * pos_j is pos_map[b][g][j] if given, else j; pos_q is the appended token's
+ * position, or without an append that of slot S_b - 1.  A sequence without
+ * keys gets out = 0.  Arguments as for kvsel_decode_attn, and:
+ *   mod          NULL (no cap, bias or window) or a host struct; slopes is fp32
+ *                [num_q_heads] on the device.
+ *   next_pos     required when pos_map is given and a token is appended.
+ *   probs        entries j >= S_b are not written; keys that are not seen get 0.
+ *   workspace    >= kvsel_kv4_decode_attn_workspace(...) bytes, zeroed before
+ *                first use; calls that may overlap need workspaces of their own.
+ * num_q_heads / num_kv_heads <= 16, batch <= 1024 (else UNSUPPORTED / INVALID).
+ * A length that is negative or does not fit the table or max_len records
+ * KVSEL_ERR_BAD_INDEX and nothing is computed for that sequence; keys on a page
+ * outside the pool record it too and are not seen.  Two launches. */
+typedef struct kvsel_score_mod {
+  float softcap;       /* 0: none */
+  const float* slopes; /* device, or NULL */
+  int32_t window;      /* 0: none */
+  int32_t n_sink;      /* with a window: the first positions stay seen */
+} kvsel_score_mod;
+KVSEL_API size_t kvsel_kv4_decode_attn_workspace(const kvsel_paged_kv4* kv, int batch, int max_len, int with_probs,
+                                                 int with_cum);
+KVSEL_API kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
+                                             int32_t* seq_lens, int batch, const void* q, const void* k_new,
+                                             const void* v_new, int32_t* pos_map, int32_t* next_pos, float scale,
+                                             const kvsel_score_mod* mod, void* out, int out_dtype, float* probs,
+                                             float* h2o_cum, int max_len, void* workspace, size_t ws_bytes,
+                                             void* stream);
+
+/* H2O eviction of the 4-bit cache by its accumulated attention weight: the
+ * selection, arguments and results of kvsel_h2o_evict, with the kept rows'
+ * codes and scales moved as they are (nothing is requantised).
+ *   workspace    >= kvsel_kv4_evict_workspace() bytes, zeroed before first use;
+ *                kvsel_h2o_link_reset applies to it.
+ * Launches: select, and with compact != 0 move and truncate. */
+KVSEL_API size_t kvsel_kv4_evict_workspace(const kvsel_paged_kv4* kv, int batch, int budget);
+KVSEL_API kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* block_table, int max_pages, int32_t* seq_lens,
+                                       int batch, float* h2o_cum, int32_t* pos_map, int max_len, int budget, int n_sink,
+                                       int window, int compact, int32_t* keep_out, int32_t* freed_pages,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
