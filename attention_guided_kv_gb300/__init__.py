@@ -121,6 +121,9 @@ _SIGS = {
                                    _vp, _i, _vp, _vp, _i, _vp, _sz, _vp]),
     "kvsel_kv4_evict_workspace": (_sz, [_PKV4, _i, _i]),
     "kvsel_kv4_evict": (_i, [_PKV4, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "kvsel_prefill_attn_workspace": (_sz, [_PKV, _i, _i]),
+    "kvsel_prefill_attn": (_i, [_PKV, _vp, _i, _vp, _i, _vp, _vp, _i, _f, _f, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp,
+                                _sz, _vp]),
     "kvsel_snapkv_select_ex": (_i, [_PKV, _vp, _i, _i, _i, _vp, _i, _f, _i, _i, ctypes.POINTER(SnapOptions), _vp,
                                     _vp, _vp, _sz, _vp]),
 }
@@ -725,4 +728,49 @@ def kvsel_kv4_evict(kv: PagedKV4, block_table, seq_lens, h2o_cum, workspace, *, 
         _check(lib().kvsel_kv4_evict(
             ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(h2o_cum), _ptr(pos_map),
             max_len, int(budget), int(n_sink), int(window), int(bool(compact)), _ptr(keep_out), _ptr(freed_pages),
+            _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# attention of prompt tokens
+# ----------------------------------------------------------------------------
+def kvsel_prefill_attn_workspace(kv: PagedKV, batch: int, total_q: int) -> int:
+    return int(lib().kvsel_prefill_attn_workspace(ctypes.byref(kv), int(batch), int(total_q)))
+
+
+def kvsel_prefill_attn(kv: PagedKV, block_table, seq_lens, q, q_off, out, workspace, *, scale=None, softcap=0.0,
+                       slopes=None, window=0, prefix=None, doc_start=None, lse=None, stream=None):
+    """Attention of packed prompt tokens (q bf16 [total][Hq][128]; sequence b's are rows q_off[b]..q_off[b + 1], the
+    last of its seq_lens[b] cached tokens) over the paged bf16 cache.
+
+    Causal; softcap: scores become softcap * tanh(score / softcap).  slopes (fp32 [Hq]): slopes[h] times the distance
+    is taken off the score.  window: only the last `window` positions are seen, and the prefix.  prefix (int32
+    [batch]): positions that every query of the sequence sees.  doc_start (int32 [total]): the first position each
+    query may see.  lse (fp32 [total][Hq]): log-sum-exp of each row's scores, -inf for a row that sees nothing.
+    """
+    batch = _table_of(block_table, seq_lens)
+    _need(q, torch.bfloat16, "q")
+    _shaped(q, (q.shape[0], kv.num_q_heads, kv.head_dim), "q")
+    total = q.shape[0]
+    _need(q_off, torch.int32, "q_off")
+    _shaped(q_off, (batch + 1,), "q_off")
+    if out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous() or out.device.type != "cuda":
+        raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor")
+    _shaped(out, q.shape, "out")
+    _need(slopes, torch.float32, "slopes", True)
+    _shaped(slopes, (kv.num_q_heads,), "slopes")
+    _need(prefix, torch.int32, "prefix", True)
+    _shaped(prefix, (batch,), "prefix")
+    _need(doc_start, torch.int32, "doc_start", True)
+    _shaped(doc_start, (total,), "doc_start")
+    _need(lse, torch.float32, "lse", True)
+    _shaped(lse, q.shape[:2], "lse")
+    _need(workspace, workspace.dtype, "workspace")
+    _same_device(block_table, seq_lens=seq_lens, q=q, q_off=q_off, out=out, slopes=slopes, prefix=prefix,
+                 doc_start=doc_start, lse=lse, workspace=workspace)
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvsel_prefill_attn(
+            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(q), _ptr(q_off), total,
+            float(kv.head_dim ** -0.5 if scale is None else scale), float(softcap), _ptr(slopes), int(window),
+            _ptr(prefix), _ptr(doc_start), _ptr(out), KVSEL_F32 if out.dtype == torch.float32 else KVSEL_BF16, _ptr(lse),
             _ptr(workspace), _nbytes(workspace), _stream(stream)))

@@ -709,7 +709,8 @@ typedef struct kvsel_paged_kv4 {
  *                calls that may overlap on the GPU need workspaces of their own.
  * Device-detected problems (bad offsets, a run beyond the table or max_len, a
  * page outside the pool) record KVSEL_ERR_BAD_INDEX; a sequence whose run does
- * not fit is left as it was.  One launch. */
+ * not fit is left as it was, a row for a page outside the pool goes nowhere.
+ * One launch. */
 KVSEL_API size_t kvsel_kv4_append_workspace(const kvsel_paged_kv4* kv, int batch);
 KVSEL_API kvsel_status kvsel_kv4_append(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
                                         int32_t* seq_lens, int batch, const int32_t* tok_off, int total_tokens,
@@ -777,6 +778,51 @@ KVSEL_API kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* block
                                        int batch, float* h2o_cum, int32_t* pos_map, int max_len, int budget, int n_sink,
                                        int window, int compact, int32_t* keep_out, int32_t* freed_pages,
                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of prompt tokens over the paged bf16 cache: a whole prompt or a
+ * chunk of one, whose K and V are in the cache already.
+ *
+ * Sequence b's queries are the packed rows [q_off[b], q_off[b + 1]); they are
+ * the last n_b of its S_b = seq_lens[b] tokens, so query i is at position
+ * p = S_b - n_b + i.  For q head h of kv head g:
+ *   t_j = scale * q . K_g[j];  t_j = softcap * tanh(t_j / softcap) if softcap > 0
+ *   t_j = t_j - slopes[h] * |p - j|                                if slopes
+ *   key j < S_b is seen if j >= doc_start[row] (if given) and either
+ *     j < prefix[b] (if given), or j <= p and, with window > 0, p - j < window
+ *   out = softmax over the seen keys times V_g;  lse = log sum exp t_j
+ * A row that sees nothing gets out = 0 and lse = -infinity.
+ *   - causal prompts: no masks; a prefix that all see (its own tokens too):
+ *     prefix; packed documents: doc_start = the position where the row's
+ *     document begins; rows to be left out: doc_start >= S_b.
+ *   - the window always keeps the prefix seen.
+ *
+ * Arguments (device pointers):
+ *   kv           paged bf16 pools (read); num_q_heads / num_kv_heads <= 16.
+ *   block_table  int32 [batch][max_pages]; seq_lens int32 [batch].
+ *   q            bf16 [total_q][num_q_heads][128]; q_off int32 [batch + 1],
+ *                non-decreasing from 0 on, at most total_q.
+ *   scale        > 0 (else INVALID_ARG);  softcap >= 0, 0: none.
+ *   slopes       fp32 [num_q_heads] or NULL;  window >= 0, 0: none.
+ *   prefix       int32 [batch] or NULL;  doc_start int32 [total_q] or NULL.
+ *   out          [total_q][num_q_heads][128], bf16 or fp32 (out_dtype); lse fp32
+ *                [total_q][num_q_heads] or NULL.  Rows past q_off[batch] stay as
+ *                they are.
+ *   workspace    >= kvsel_prefill_attn_workspace() bytes, zeroed before first
+ *                use; calls that may overlap on the GPU need their own.
+ * Slots at or past seq_lens[b] never matter, whatever their pages hold.  A NaN or
+ * infinity in the V row of a live key may reach every query of its sequence (0
+ * times it is NaN); in a K row it reaches the queries that see the key.
+ * Bad offsets or a length beyond the table record KVSEL_ERR_BAD_INDEX and leave
+ * that sequence's rows as they are; a page outside the pool records it, and the
+ * sequence's results are then unspecified.  One launch, and a second one that
+ * joins where few queries are split over their keys. */
+KVSEL_API size_t kvsel_prefill_attn_workspace(const kvsel_paged_kv* kv, int batch, int total_q);
+KVSEL_API kvsel_status kvsel_prefill_attn(const kvsel_paged_kv* kv, const int32_t* block_table, int max_pages,
+                                          const int32_t* seq_lens, int batch, const void* q, const int32_t* q_off,
+                                          int total_q, float scale, float softcap, const float* slopes, int window,
+                                          const int32_t* prefix, const int32_t* doc_start, void* out, int out_dtype,
+                                          float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
