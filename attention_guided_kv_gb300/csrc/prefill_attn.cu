@@ -18,6 +18,8 @@
 //           O += P V (P from tensor memory, V as it lies: d contiguous)
 //   warps 0-3 and 4-7  one tile each, one thread a row: S out of tensor memory,
 //           mask, maximum, exponentials, P back into the columns S had
+// A row's 128 scores stay in registers: the softmax warps take 216 each
+// (setmaxnreg), warps 8-11 give theirs up.
 // Tensor memory is full: 2 x 128 columns of S / P and 2 x 128 of O.  While one
 // tile's rows are in the exponentials the other tile's products run.
 // Few rows (a chunk of a few tokens): the key tiles are split over several
@@ -35,7 +37,7 @@ constexpr int kPfD = 128;
 constexpr int kPfKeys = 128;
 constexpr int kPfTileRows = 128;
 constexpr int kPfStages = 2;
-constexpr int kPfThreads = 320;
+constexpr int kPfThreads = 384;
 constexpr int kPfTileBytes = kPfKeys * kPfD * 2;        // 32 KB: two slabs of 64 columns
 constexpr int kPfSlab = kPfKeys * 128;                  // 16 KB
 constexpr int kPfSmem = 1024 + (2 + 2 * kPfStages) * kPfTileBytes;
@@ -64,6 +66,11 @@ struct PrefillParams {
 __device__ __forceinline__ float pf_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 __device__ __forceinline__ float pf_rcp(float x) {
@@ -109,6 +116,56 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 consecutive fp32 columns of this thread's TMEM lane, not waited for.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Values of asynchronous loads may be used only after the wait: this ties 32
+// of them to it (volatile statements keep their order).
+__device__ __forceinline__ void tmem_tie32(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+// All 128 fp32 columns of this thread's row of S.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32_async(taddr + 32 * c, v + 32 * c);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_tie32(v + 32 * c);
+}
+
+// Two fp32 operations an instruction: (x, y) op ...
+__device__ __forceinline__ void fma2(float& dx, float& dy, float ax, float ay, float bx, float by, float cx, float cy) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(dx), "=f"(dy)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by), "f"(cx), "f"(cy));
+}
+__device__ __forceinline__ void mul2(float& dx, float& dy, float ax, float ay, float bx, float by) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(dx), "=f"(dy)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void add2(float& dx, float& dy, float ax, float ay, float bx, float by) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(dx), "=f"(dy)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+
+// Bits lo..hi (inclusive, both clipped to 0..31) of a word.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const uint32_t from = lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+  const uint32_t to = hi >= 31 ? ~0u : hi < 0 ? 0u : ~0u >> (31 - hi);
+  return from & to;
+}
+
 // Key tiles that some row of a CTA sees: [a0, a1) and [b0, b1), disjoint, a first.
 struct KeyTiles {
   int a0, a1, b0, b1;
@@ -126,7 +183,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   uint8_t* sK = smem + 2 * kPfTileBytes;
   uint8_t* sV = sK + kPfStages * kPfTileBytes;
   __shared__ uint64_t k_full[kPfStages], v_full[kPfStages], k_empty[kPfStages], v_empty[kPfStages];
-  __shared__ uint64_t s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_b, s_tile, s_rng[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -200,18 +257,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       atomicMax(&s_rng[3], b_hi);
     }
   }
-  // ---- Q rows, 128-byte swizzled; rows past the end are zero
   const int tiles = rows - row0 > kPfTileRows ? 2 : 1;
-  for (int idx = tid; idx < tiles * kPfTileRows * 16; idx += kPfThreads) {
-    const int r = idx >> 4, ch = idx & 15, gr = row0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (gr < rows) {
-      const int i = gr / P.G, h = gr - i * P.G;
-      v = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
-    }
-    *reinterpret_cast<uint4*>(sQ + (r >> 7) * kPfTileBytes + (ch >> 3) * kPfSlab + (r & 127) * 128 +
-                              (((ch & 7) ^ (r & 7)) << 4)) = v;
-  }
   if (tid == 0) {
     for (int s = 0; s < kPfStages; ++s) {
       mbar_init(smem_u32(&k_full[s]), 1);
@@ -223,10 +269,10 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       mbar_init(smem_u32(&s_full[t]), 1);
       mbar_init(smem_u32(&p_full[t]), kPfTileRows);
       mbar_init(smem_u32(&o_full[t]), 1);
+      mbar_init(smem_u32(&q_full[t]), kPfTileRows);
     }
     mbar_fence_init();
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q stores -> tensor-core reads
   if (warp == 9) {
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
@@ -253,6 +299,9 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const int all = kt.count();
   const int i0 = int((long long)split * all / P.splits), n = int((long long)(split + 1) * all / P.splits) - i0;
 
+  // registers: 256 x 216 + 128 x 72 = 64512, the 384 x 168 of the launch
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 8) {
     // ---- producer: a lane per page of the tile
     const int32_t* bt = P.block_table + (size_t)b * P.max_pages;
@@ -324,8 +373,11 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
     if (n > 0) {
       ok = wait(&k_full[0], 0);
+      for (int t = 0; t < tiles && ok; ++t) {
+        ok = wait(&q_full[t], 0);
+        if (ok) qk(t, 0);
+      }
       if (ok) {
-        for (int t = 0; t < tiles; ++t) qk(t, 0);
         // a stage is handed back only if another tile comes into it: nothing arrives after the CTA is gone
         if (lane == 0 && n > kPfStages) umma_commit(smem_u32(&k_empty[0]));
         __syncwarp();
@@ -371,14 +423,31 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       __syncwarp();
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax: one thread a row
     const int t = warp >> 2;
+    // this tile's Q rows, 128-byte swizzled; rows past the end are zero
+    if (t < tiles && n > 0) {
+#pragma unroll 4
+      for (int k = 0; k < 16; ++k) {
+        const int r = (tid & 127) / 16 + 8 * k, ch = tid & 15, gr = row0 + t * kPfTileRows + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (gr < rows) {
+          const int i = gr / P.G, h = gr - i * P.G;
+          v = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
+        }
+        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q stores -> tensor-core reads
+      mbar_arrive(smem_u32(&q_full[t]));
+    }
     const uint32_t lane_addr = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_addr = tbase + lane_addr + t * 128, o_addr = tbase + lane_addr + 256 + t * 128;
     float m = -INFINITY, l = 0.f;
-    const float sc = kCap ? 2.f * kPfLog2e * P.scale / P.softcap : P.scale * kPfLog2e;
-    const float cap2 = P.softcap * kPfLog2e;
+    const float sc = P.scale * kPfLog2e, cap2 = P.softcap * kPfLog2e;
+    const float cap_in = kCap ? P.scale / P.softcap : 0.f;
     const float slope2 = kBias && in ? __ldg(P.slopes + head) * kPfLog2e : 0.f;
     bool ok = true;
     if (t < tiles) {
@@ -391,32 +460,57 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         tc_fence_after();
         float x[kPfKeys];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, reinterpret_cast<float(&)[32]>(x[32 * c]));
+        tmem_ld128(s_addr, x);
         const int t0 = kt.key0(i0 + i);
+        const int clo = jlo < t0 ? 0 : jlo - t0, chi = jhi < t0 ? -1 : jhi - t0;      // seen: clo..chi
+        const int dlo = jdoc < t0 ? 0 : jdoc - t0, dhi = jpre - t0;                   // and dlo..dhi - 1
+        const bool whole = !in || (clo == 0 && chi >= kPfKeys - 1) || (dlo == 0 && dhi >= kPfKeys);
         if (kCap) {
+          // softcap tanh(u), u = scale q.k / softcap.  Scores far below the cap (|u| < 0.5, the usual
+          // case): an odd polynomial fitted to it there, 1.3e-7 off at most; it runs on the FMA pipe, which
+          // has time, where the exponential and the reciprocal would triple the load of the unit that bounds
+          // this kernel.
+          float top = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-          for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-2.f * cap2, pf_rcp(pf_ex2(x[c] * sc) + 1.f), cap2);
+          for (int c = 2; c < kPfKeys; c += 2) top = max3(top, fabsf(x[c]), fabsf(x[c + 1]));
+          if (__all_sync(0xffffffffu, top * cap_in < 0.5f)) {
+#pragma unroll
+            for (int c = 0; c < kPfKeys; c += 2) {
+              float u0, u1, w0, w1, y0, y1;
+              mul2(u0, u1, x[c], x[c + 1], cap_in, cap_in);
+              mul2(w0, w1, u0, u1, u0, u1);
+              mul2(u0, u1, u0, u1, cap2, cap2);
+              fma2(y0, y1, w0, w1, -0.043372482f, -0.043372482f, 0.131451458f, 0.131451458f);
+              fma2(y0, y1, y0, y1, w0, w1, -0.333206564f, -0.333206564f);
+              fma2(y0, y1, y0, y1, w0, w1, 0.999997675f, 0.999997675f);
+              mul2(x[c], x[c + 1], u0, u1, y0, y1);
+            }
+          } else {
+            const float k = 2.f * kPfLog2e * cap_in;
+#pragma unroll
+            for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-2.f * cap2, pf_rcp(pf_ex2(x[c] * k) + 1.f), cap2);
+          }
         } else if (kBias) {
 #pragma unroll
-          for (int c = 0; c < kPfKeys; ++c) x[c] *= sc;
+          for (int c = 0; c < kPfKeys; c += 2) mul2(x[c], x[c + 1], x[c], x[c + 1], sc, sc);
         }
         if (kBias) {
           const float d = float(pos - t0);
 #pragma unroll
           for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-slope2, fabsf(d - float(c)), x[c]);
         }
-        const int clo = jlo < t0 ? 0 : jlo - t0, chi = jhi < t0 ? -1 : jhi - t0;      // seen: clo..chi
-        const int dlo = jdoc < t0 ? 0 : jdoc - t0, dhi = jpre - t0;                   // and dlo..dhi - 1
-        const bool whole = !in || (clo == 0 && chi >= kPfKeys - 1) || (dlo == 0 && dhi >= kPfKeys);
         if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
-          for (int c = 0; c < kPfKeys; ++c)
-            x[c] = (c >= clo && c <= chi) || (c >= dlo && c < dhi) ? x[c] : -INFINITY;
-        }
-        float mx = fmaxf(x[0], x[1]);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = in ? bit_range(clo - 32 * w, chi - 32 * w) | bit_range(dlo - 32 * w, dhi - 1 - 32 * w) : 0u;
 #pragma unroll
-        for (int c = 2; c < kPfKeys; c += 2) mx = fmaxf(mx, fmaxf(x[c], x[c + 1]));
+            for (int c = 0; c < 32; ++c) x[32 * w + c] = (bits >> c) & 1u ? x[32 * w + c] : -INFINITY;
+          }
+        }
+        float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < kPfKeys; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (!kCap && !kBias) mx *= sc;                   // sc > 0
         const bool grow = mx > m + kPfSlack || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, grow)) {
@@ -442,12 +536,12 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           uint32_t u[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const int c = 64 * hf + 2 * k;
-            const float p0 = pf_ex2(kCap || kBias ? x[c] - use : fmaf(x[c], sc, -use));
-            const float p1 = pf_ex2(kCap || kBias ? x[c + 1] - use : fmaf(x[c + 1], sc, -use));
-            sum[k & 1] += p0;
-            sum[2 + (k & 1)] += p1;
-            u[k] = pack_bf16x2(p0, p1);
+            float &y0 = x[64 * hf + 2 * k], &y1 = x[64 * hf + 2 * k + 1];
+            if (kCap || kBias) add2(y0, y1, y0, y1, -use, -use);
+            else fma2(y0, y1, y0, y1, sc, sc, -use, -use);
+            const float e0 = pf_ex2(y0), e1 = pf_ex2(y1);
+            add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
+            u[k] = pack_bf16x2(e0, e1);
           }
           tmem_st32(s_addr + 32 * hf, u);
         }
