@@ -79,6 +79,13 @@ __device__ __forceinline__ float pf_rcp(float x) {
   return y;
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Descriptor of V as the right operand (K = keys x N = dims, N contiguous,
 // 128-byte swizzle): 64-dim slabs kPfSlab apart (LBO), 8-key groups 1024 bytes
 // apart (SBO).
@@ -186,7 +193,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   __shared__ uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_b, s_tile, s_rng[4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // ---- which rows: CTAs in the order (tile, split, kv head), a sequence's last tile first
   const int kvh = blockIdx.x % P.Hkv, rest = blockIdx.x / P.Hkv;
@@ -280,7 +287,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = s_tmem;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, s_tmem, 0);
   KeyTiles kt{0, 0, 0, 0};
   {
     if (s_rng[1] > 0) {
@@ -359,13 +366,18 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       tc_fence_after();
       return got;
     };
+    // The operands are the same in every lane and one elected lane issues: a lane picked by its
+    // index would have the compiler serialise each instruction over the lanes (80 to 100 cycles
+    // each instead of the 64 that it computes).
+    const uint64_t dq = umma_desc_sw128(smem_u32(sQ)), dk = umma_desc_sw128(smem_u32(sK)), dv = umma_desc_v(smem_u32(sV));
     auto qk = [&](int t, int i) {
-      const uint32_t a = smem_u32(sQ) + t * kPfTileBytes, k = smem_u32(sK) + (i % kPfStages) * kPfTileBytes;
-      if (lane == 0) {
+      const uint64_t a = dq + uint64_t(t * (kPfTileBytes >> 4)), k = dk + uint64_t((i % kPfStages) * (kPfTileBytes >> 4));
+      const uint32_t d = tbase + t * 128;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t o = uint32_t(kk >> 2) * kPfSlab + uint32_t(kk & 3) * 32;
-          umma_bf16(tbase + t * 128, umma_desc_sw128(a + o), umma_desc_sw128(k + o), id_qk, kk > 0);
+          const uint64_t o = uint64_t(((kk >> 2) * kPfSlab + (kk & 3) * 32) >> 4);
+          umma_bf16(d, a + o, k + o, id_qk, kk > 0);
         }
         umma_commit(smem_u32(&s_full[t]));
       }
@@ -379,7 +391,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       if (ok) {
         // a stage is handed back only if another tile comes into it: nothing arrives after the CTA is gone
-        if (lane == 0 && n > kPfStages) umma_commit(smem_u32(&k_empty[0]));
+        if (n > kPfStages && elect_one()) umma_commit(smem_u32(&k_empty[0]));
         __syncwarp();
       }
     }
@@ -401,12 +413,13 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       for (int t = 0; t < tiles && ok; ++t) {
         ok = wait(&p_full[t], i & 1);
         if (!ok) break;
-        if (lane == 0) {
-          const uint32_t v = smem_u32(sV) + s * kPfTileBytes;
+        const uint64_t v = dv + uint64_t(s * (kPfTileBytes >> 4));
+        const uint32_t po = tbase + t * 128, d = po + 256;
+        const bool first = i == 0, last = i + 1 == n;
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tbase + 256 + t * 128, tbase + t * 128 + kk * 8, umma_desc_v(v + kk * 2048), id_pv, i > 0 || kk > 0);
-          if (i + 1 == n) umma_commit(smem_u32(&o_full[t]));
+          for (int kk = 0; kk < 8; ++kk) umma_bf16_ts(d, po + kk * 8, v + uint64_t(kk * (2048 >> 4)), id_pv, !first || kk > 0);
+          if (last) umma_commit(smem_u32(&o_full[t]));
         }
         __syncwarp();
         if (i + 1 < n) {
@@ -417,10 +430,8 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           qk(t, i + 1);
         }
       }
-      if (lane == 0 && ok) {
-        if (i + kPfStages < n) umma_commit(smem_u32(&v_empty[s]));
-        if (i + 1 + kPfStages < n) umma_commit(smem_u32(&k_empty[(i + 1) % kPfStages]));
-      }
+      if (ok && i + kPfStages < n && elect_one()) umma_commit(smem_u32(&v_empty[s]));
+      if (ok && i + 1 + kPfStages < n && elect_one()) umma_commit(smem_u32(&k_empty[(i + 1) % kPfStages]));
       __syncwarp();
     }
   }
@@ -448,6 +459,9 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     float m = -INFINITY, l = 0.f;
     const float sc = P.scale * kPfLog2e, cap2 = P.softcap * kPfLog2e;
     const float cap_in = kCap ? P.scale / P.softcap : 0.f;
+    // softcap log2(e) tanh(cap_in x) ~ x (pc0 + pc1 x^2 + pc2 x^4 + pc3 x^6)
+    const float ci2 = cap_in * cap_in, pc0 = 0.999997675f * cap2 * cap_in, pc1 = -0.333206564f * cap2 * cap_in * ci2;
+    const float pc2 = 0.131451458f * cap2 * cap_in * ci2 * ci2, pc3 = -0.043372482f * cap2 * cap_in * ci2 * ci2 * ci2;
     const float slope2 = kBias && in ? __ldg(P.slopes + head) * kPfLog2e : 0.f;
     bool ok = true;
     if (t < tiles) {
@@ -465,30 +479,36 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int clo = jlo < t0 ? 0 : jlo - t0, chi = jhi < t0 ? -1 : jhi - t0;      // seen: clo..chi
         const int dlo = jdoc < t0 ? 0 : jdoc - t0, dhi = jpre - t0;                   // and dlo..dhi - 1
         const bool whole = !in || (clo == 0 && chi >= kPfKeys - 1) || (dlo == 0 && dhi >= kPfKeys);
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool part = !__all_sync(0xffffffffu, whole);
+        if (part) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            seen[w] = in ? bit_range(clo - 32 * w, chi - 32 * w) | bit_range(dlo - 32 * w, dhi - 1 - 32 * w) : 0u;
+        }
+        // softcap tanh(u), u = scale q.k / softcap.  Scores far below the cap (|u| < 0.5, the usual case): an odd
+        // polynomial fitted to it there, 1.3e-7 off at most, on the FMA pipe, which has time, where the
+        // exponential and the reciprocal would triple the load of the special-function unit.
+        bool poly = false;
         if (kCap) {
-          // softcap tanh(u), u = scale q.k / softcap.  Scores far below the cap (|u| < 0.5, the usual
-          // case): an odd polynomial fitted to it there, 1.3e-7 off at most; it runs on the FMA pipe, which
-          // has time, where the exponential and the reciprocal would triple the load of the unit that bounds
-          // this kernel.
           float top = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
           for (int c = 2; c < kPfKeys; c += 2) top = max3(top, fabsf(x[c]), fabsf(x[c + 1]));
-          if (__all_sync(0xffffffffu, top * cap_in < 0.5f)) {
-#pragma unroll
-            for (int c = 0; c < kPfKeys; c += 2) {
-              float u0, u1, w0, w1, y0, y1;
-              mul2(u0, u1, x[c], x[c + 1], cap_in, cap_in);
-              mul2(w0, w1, u0, u1, u0, u1);
-              mul2(u0, u1, u0, u1, cap2, cap2);
-              fma2(y0, y1, w0, w1, -0.043372482f, -0.043372482f, 0.131451458f, 0.131451458f);
-              fma2(y0, y1, y0, y1, w0, w1, -0.333206564f, -0.333206564f);
-              fma2(y0, y1, y0, y1, w0, w1, 0.999997675f, 0.999997675f);
-              mul2(x[c], x[c + 1], u0, u1, y0, y1);
-            }
-          } else {
+          poly = __all_sync(0xffffffffu, top * cap_in < 0.5f);
+          if (!poly) {
             const float k = 2.f * kPfLog2e * cap_in;
 #pragma unroll
             for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-2.f * cap2, pf_rcp(pf_ex2(x[c] * k) + 1.f), cap2);
+          } else if (kBias) {
+#pragma unroll
+            for (int c = 0; c < kPfKeys; c += 2) {
+              float z0, z1, y0, y1;
+              mul2(z0, z1, x[c], x[c + 1], x[c], x[c + 1]);
+              fma2(y0, y1, z0, z1, pc3, pc3, pc2, pc2);
+              fma2(y0, y1, y0, y1, z0, z1, pc1, pc1);
+              fma2(y0, y1, y0, y1, z0, z1, pc0, pc0);
+              mul2(x[c], x[c + 1], x[c], x[c + 1], y0, y1);
+            }
           }
         } else if (kBias) {
 #pragma unroll
@@ -499,19 +519,20 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
           for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-slope2, fabsf(d - float(c)), x[c]);
         }
-        if (!__all_sync(0xffffffffu, whole)) {
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (part) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = in ? bit_range(clo - 32 * w, chi - 32 * w) | bit_range(dlo - 32 * w, dhi - 1 - 32 * w) : 0u;
+          for (int c = 0; c < kPfKeys; c += 2)
+            mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], (seen[c >> 5] >> (c & 31)) & 1u ? x[c] : -INFINITY,
+                                     (seen[c >> 5] >> (c & 31)) & 2u ? x[c + 1] : -INFINITY);
+        } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[32 * w + c] = (bits >> c) & 1u ? x[32 * w + c] : -INFINITY;
-          }
+          for (int c = 0; c < kPfKeys; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
         }
-        float mx4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int c = 4; c < kPfKeys; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         if (!kCap && !kBias) mx *= sc;                   // sc > 0
+        if (kCap && !kBias && poly && mx != -INFINITY)   // x is still raw, and the polynomial is increasing
+          mx *= fmaf(fmaf(fmaf(mx * mx, pc3, pc2), mx * mx, pc1), mx * mx, pc0);
         const bool grow = mx > m + kPfSlack || (m == -INFINITY && mx > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float corr = grow ? pf_ex2(m - mx) : 1.f;
@@ -534,12 +555,33 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t u[32];
+          if (kCap && !kBias && poly) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float &x0 = x[64 * hf + 2 * k], &x1 = x[64 * hf + 2 * k + 1];
+              float z0, z1, y0, y1;
+              mul2(z0, z1, x0, x1, x0, x1);
+              fma2(y0, y1, z0, z1, pc3, pc3, pc2, pc2);
+              fma2(y0, y1, y0, y1, z0, z1, pc1, pc1);
+              fma2(y0, y1, y0, y1, z0, z1, pc0, pc0);
+              fma2(x0, x1, x0, x1, y0, y1, -use, -use);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float &x0 = x[64 * hf + 2 * k], &x1 = x[64 * hf + 2 * k + 1];
+              if (kCap || kBias) add2(x0, x1, x0, x1, -use, -use);
+              else fma2(x0, x1, x0, x1, sc, sc, -use, -use);
+            }
+          }
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            float &y0 = x[64 * hf + 2 * k], &y1 = x[64 * hf + 2 * k + 1];
-            if (kCap || kBias) add2(y0, y1, y0, y1, -use, -use);
-            else fma2(y0, y1, y0, y1, sc, sc, -use, -use);
-            const float e0 = pf_ex2(y0), e1 = pf_ex2(y1);
+            const int c = 64 * hf + 2 * k;
+            float e0 = pf_ex2(x[c]), e1 = pf_ex2(x[c + 1]);
+            if (part) {
+              e0 = (seen[c >> 5] >> (c & 31)) & 1u ? e0 : 0.f;
+              e1 = (seen[c >> 5] >> (c & 31)) & 2u ? e1 : 0.f;
+            }
             add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
             u[k] = pack_bf16x2(e0, e1);
           }
