@@ -49,12 +49,15 @@ __device__ __forceinline__ uint32_t q4_scale_bits(float hi_v, float lo_v) {
   return u < (27u << 7) ? 0u : u;       // 2^-100 has exponent field 27
 }
 
-// The code of x in a group of minimum z and scale s > 0 (inv ~ 1 / s).
-__device__ __forceinline__ uint32_t q4_code(float x, float z, float s, float inv) {
+// The code of x >= z in a group of minimum z and scale s > 0 (inv ~ 1 / s), as
+// a float.  Adding 1.5 * 2^23 rounds to an integer, ties to even.  No clamp:
+// s is at least (1 - 2^-8) / 15 of the range, so the quotient is below 15.1.
+__device__ __forceinline__ float q4_code(float x, float z, float s, float half_s, float inv) {
+  constexpr float kMagic = 12582912.f;
   const float r = __fsub_rn(x, z);
-  float n = rintf(r * inv);
+  float n = __fsub_rn(__fmaf_rn(r, inv, kMagic), kMagic);
   const float d = __fmaf_rn(-n, s, r);
-  if (fabsf(d) >= 0.5f * s) {           // on or past a border: settle it exactly
+  if (fabsf(d) >= half_s) {             // on or past a border: settle it exactly
     float err;
     const float rr = two_sum(x, -z, err);
     const float f = d > 0.0f ? n : n - 1.0f;
@@ -62,7 +65,7 @@ __device__ __forceinline__ uint32_t q4_code(float x, float z, float s, float inv
     const bool up = e > 0.0f || (e == 0.0f && (int(f) & 1));
     n = up ? f + 1.0f : f;
   }
-  return uint32_t(fminf(fmaxf(n, 0.0f), 15.0f));
+  return n;
 }
 
 // One group spread over 32 / NV neighbouring lanes of NV values each (bf16
@@ -99,10 +102,16 @@ __device__ __forceinline__ uint32_t q4_group(const uint32_t (&raw)[NV / 2], uint
   sz = sb | (__float_as_uint(lo) & 0xFFFF0000u);
   if (sb == 0u) return 0u;
   const float s = __uint_as_float(sb << 16);
-  const float inv = __fdividef(1.0f, s);
+  const float inv = __fdividef(1.0f, s), half_s = 0.5f * s;
+  // four codes at a time as one integer below 2^16 in a float's mantissa
   uint32_t codes = 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) codes |= q4_code(x[i], lo, s, inv) << (4 * i);
+  for (int q = 0; q < NV / 4; ++q) {
+    float v = 8388608.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v = __fmaf_rn(q4_code(x[4 * q + i], lo, s, half_s, inv), float(1 << (4 * i)), v);
+    codes |= (__float_as_uint(v) & 0xFFFFu) << (16 * q);
+  }
   return codes;
 }
 

@@ -22,7 +22,8 @@
 namespace kvsel {
 
 constexpr int kQaThreads = 256;
-constexpr int kQaRows = kQaThreads / 16;  // (token, kv head) rows a CTA takes at a time
+constexpr int kQaUnroll = 2;                          // rows a thread has in flight
+constexpr int kQaRows = kQaThreads / 16 * kQaUnroll;  // (token, kv head) rows a CTA takes at a time
 
 struct Kv4Params {
   uint8_t* codes[2];   // K, V
@@ -70,44 +71,53 @@ __device__ __forceinline__ int run_of(const Kv4Params& P, int b) {
 
 __global__ void __launch_bounds__(kQaThreads) kv4_append_kernel(const AppendParams P) {
   const int tid = threadIdx.x, l16 = tid & 15;
-  const long long rows = (long long)P.total * P.Hkv;
+  const uint32_t rows = uint32_t(P.total) * uint32_t(P.Hkv);   // < 2^31: checked on the host
   const int page_mask = (1 << P.page_lg) - 1;
   const long long capacity = (long long)P.max_pages << P.page_lg;
+  const int end = __ldg(P.tok_off + P.batch);
 #pragma unroll 1
-  for (long long r0 = (long long)blockIdx.x * kQaRows; r0 < rows; r0 += (long long)gridDim.x * kQaRows) {
-    const long long r = r0 + (tid >> 4);
-    const bool in = r < rows;
-    const long long rc = in ? r : rows - 1;   // every lane takes part in the shuffles
-    const uint4 kx = __ldcs(P.k + rc * 16 + l16), vx = __ldcs(P.v + rc * 16 + l16);
-    const int t = int(rc / P.Hkv), g = int(rc - (long long)t * P.Hkv);
-    const int b = owner_of(P.tok_off, P.batch, t);
-    const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
-    const int S = __ldcg(P.seq_lens + b);
-    bool ok = n >= 0 && at >= 0 && at < n && S >= 0 && (long long)S + n <= capacity &&
-              (P.max_len == 0 || (long long)S + n <= P.max_len);
-    long long row = 0;
-    const int slot = S + at;
-    if (ok) {
-      const int phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
-      ok = unsigned(phys) < unsigned(P.num_pages);
-      row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
-    }
-    const bool tail = t >= __ldg(P.tok_off + P.batch);  // rows behind the last sequence are nobody's
-    if (in && !ok && !tail && l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
-    uint32_t sz[2], codes[2];
-    const uint32_t kr[4] = {kx.x, kx.y, kx.z, kx.w}, vr[4] = {vx.x, vx.y, vx.z, vx.w};
-    codes[0] = q4_group<8>(kr, sz[0]);
-    codes[1] = q4_group<8>(vr, sz[1]);
-    if (!in || !ok) continue;
+  for (uint32_t r0 = blockIdx.x * kQaRows; r0 < rows; r0 += gridDim.x * kQaRows) {
+    uint4 kx[kQaUnroll], vx[kQaUnroll];
+    uint32_t rc[kQaUnroll];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      reinterpret_cast<uint32_t*>(P.codes[side] + row * kQ4CodeBytes)[l16] = codes[side];
-      if ((l16 & 3) == 0) reinterpret_cast<uint32_t*>(P.scales[side] + row * kQ4ScaleBytes)[l16 >> 2] = sz[side];
+    for (int u = 0; u < kQaUnroll; ++u) {
+      rc[u] = min(r0 + u * (kQaThreads / 16) + (tid >> 4), rows - 1);   // every lane takes part in the shuffles
+      kx[u] = __ldcs(P.k + size_t(rc[u]) * 16 + l16);
+      vx[u] = __ldcs(P.v + size_t(rc[u]) * 16 + l16);
     }
-    if (l16 == 0) {
-      const size_t at_row = ((size_t)b * P.Hkv + g) * P.max_len + slot;
-      if (P.pos_map) P.pos_map[at_row] = __ldcg(P.next_pos + b) + at;
-      if (P.cum) P.cum[at_row] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kQaUnroll; ++u) {
+      const bool in = r0 + u * (kQaThreads / 16) + (tid >> 4) < rows;
+      const int t = int(rc[u] / uint32_t(P.Hkv)), g = int(rc[u] - uint32_t(t) * P.Hkv);
+      const int b = owner_of(P.tok_off, P.batch, t);
+      const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
+      const int S = __ldcg(P.seq_lens + b);
+      bool ok = n >= 0 && at >= 0 && at < n && S >= 0 && (long long)S + n <= capacity &&
+                (P.max_len == 0 || (long long)S + n <= P.max_len);
+      long long row = 0;
+      const int slot = S + at;
+      if (ok) {
+        const int phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
+        ok = unsigned(phys) < unsigned(P.num_pages);
+        row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+      }
+      // rows behind the last sequence are nobody's
+      if (in && !ok && t < end && l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+      uint32_t sz[2], codes[2];
+      const uint32_t kr[4] = {kx[u].x, kx[u].y, kx[u].z, kx[u].w}, vr[4] = {vx[u].x, vx[u].y, vx[u].z, vx[u].w};
+      codes[0] = q4_group<8>(kr, sz[0]);
+      codes[1] = q4_group<8>(vr, sz[1]);
+      if (!in || !ok) continue;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        reinterpret_cast<uint32_t*>(P.codes[side] + row * kQ4CodeBytes)[l16] = codes[side];
+        if ((l16 & 3) == 0) reinterpret_cast<uint32_t*>(P.scales[side] + row * kQ4ScaleBytes)[l16 >> 2] = sz[side];
+      }
+      if (l16 == 0) {
+        const size_t at_row = ((size_t)b * P.Hkv + g) * P.max_len + slot;
+        if (P.pos_map) P.pos_map[at_row] = __ldcg(P.next_pos + b) + at;
+        if (P.cum) P.cum[at_row] = 0.0f;
+      }
     }
   }
   // the lengths change once every CTA has read them
@@ -134,43 +144,59 @@ __global__ void __launch_bounds__(kQaThreads) kv4_append_kernel(const AppendPara
 
 __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P) {
   const int tid = threadIdx.x, l16 = tid & 15;
-  const long long rows = (long long)P.total * P.Hkv;
+  const uint32_t rows = uint32_t(P.total) * uint32_t(P.Hkv);
   const int page_mask = (1 << P.page_lg) - 1;
   const long long capacity = (long long)P.max_pages << P.page_lg;
+  const int end = __ldg(P.tok_off + P.batch);
 #pragma unroll 1
-  for (long long r = (long long)blockIdx.x * kQaRows + (tid >> 4); r < rows; r += (long long)gridDim.x * kQaRows) {
-    const int t = int(r / P.Hkv), g = int(r - (long long)t * P.Hkv);
-    if (t >= __ldg(P.tok_off + P.batch)) continue;  // rows behind the last sequence stay as they are
-    const int b = owner_of(P.tok_off, P.batch, t);
-    const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
-    const int S = __ldg(P.seq_lens + b), first = P.start ? __ldg(P.start + b) : 0;
-    const long long slot = (long long)first + at;
-    bool ok = n >= 0 && at >= 0 && at < n && first >= 0 && slot < S && slot < capacity;
-    int phys = -1;
-    if (ok) {
-      phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
-      ok = unsigned(phys) < unsigned(P.num_pages);
-    }
-    if (!ok) {
-      if (l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
-      continue;
-    }
-    const long long row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
-    uint32_t codes[2], sz[2];
+  for (uint32_t r0 = blockIdx.x * kQaRows; r0 < rows; r0 += gridDim.x * kQaRows) {
+    uint32_t codes[kQaUnroll][2], sz[kQaUnroll][2], rr[kQaUnroll];
+    bool ok[kQaUnroll];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      codes[side] = __ldg(reinterpret_cast<const uint32_t*>(P.codes[side] + row * kQ4CodeBytes) + l16);
-      sz[side] = __ldg(reinterpret_cast<const uint32_t*>(P.scales[side] + row * kQ4ScaleBytes) + (l16 >> 2));
+    for (int u = 0; u < kQaUnroll; ++u) {
+      rr[u] = r0 + u * (kQaThreads / 16) + (tid >> 4);
+      const int t = int(rr[u] / uint32_t(P.Hkv)), g = int(rr[u] - uint32_t(t) * P.Hkv);
+      ok[u] = rr[u] < rows && t < end;    // rows behind the last sequence stay as they are
+      if (!ok[u]) continue;
+      const int b = owner_of(P.tok_off, P.batch, t);
+      const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
+      const int S = __ldg(P.seq_lens + b), first = P.start ? __ldg(P.start + b) : 0;
+      const long long slot = (long long)first + at;
+      bool good = n >= 0 && at >= 0 && at < n && first >= 0 && slot < S && slot < capacity;
+      int phys = -1;
+      if (good) {
+        phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
+        good = unsigned(phys) < unsigned(P.num_pages);
+      }
+      if (!good) {
+        if (l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+        ok[u] = false;
+        continue;
+      }
+      const long long row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        codes[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.codes[side] + row * kQ4CodeBytes) + l16);
+        sz[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.scales[side] + row * kQ4ScaleBytes) + (l16 >> 2));
+      }
     }
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const float s = bf16lo_to_f32(sz[side]), z = bf16hi_to_f32(sz[side]);
-      float x[8];
+    for (int u = 0; u < kQaUnroll; ++u) {
+      if (!ok[u]) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(float((codes[side] >> (4 * i)) & 15u), s, z);
-      const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                 pack_bf16x2(x[6], x[7]));
-      __stcs((side ? P.v : P.k) + r * 16 + l16, o);
+      for (int side = 0; side < 2; ++side) {
+        const float s = bf16lo_to_f32(sz[u][side]), z = bf16hi_to_f32(sz[u][side]);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // the code in the mantissa of 2^23 + n, without a conversion
+          const float n = __uint_as_float(0x4B000000u | ((codes[u][side] >> (4 * i)) & 15u)) - 8388608.f;
+          x[i] = fmaf(n, s, z);
+        }
+        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                   pack_bf16x2(x[6], x[7]));
+        __stcs((side ? P.v : P.k) + size_t(rr[u]) * 16 + l16, o);
+      }
     }
   }
 }
@@ -351,6 +377,8 @@ extern "C" kvsel_status kvsel_kv4_append(const kvsel_paged_kv4* kv, const int32_
     return fail(KVSEL_ERR_INVALID_ARG, fn + "k and v (16-byte aligned) are required");
   if (!workspace || !aligned(workspace, 256) || ws_bytes < kvsel_kv4_append_workspace(kv, batch))
     return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace of kvsel_kv4_append_workspace() bytes is required");
+  if ((long long)total_tokens * kv->num_kv_heads >= (1ll << 31) - (1 << 20))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "total_tokens * num_kv_heads must be below 2^31 - 2^20");
   if (total_tokens == 0) return KVSEL_OK;
   AppendParams P;
   fill(P, kv, block_table, max_pages, seq_lens, batch, tok_off, total_tokens, workspace);
@@ -381,6 +409,8 @@ extern "C" kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t*
     return fail(KVSEL_ERR_INVALID_ARG, fn + "k_out and v_out (16-byte aligned) are required");
   if (!workspace || !aligned(workspace, 256) || ws_bytes < kStatusBytes)
     return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace of at least 256 bytes is required");
+  if ((long long)total_tokens * kv->num_kv_heads >= (1ll << 31) - (1 << 20))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "total_tokens * num_kv_heads must be below 2^31 - 2^20");
   if (total_tokens == 0) return KVSEL_OK;
   ReadParams P;
   fill(P, kv, block_table, max_pages, const_cast<int32_t*>(seq_lens), batch, tok_off, total_tokens, workspace);

@@ -27,11 +27,14 @@
 //   through a private shared-memory ring with cp.async (no barrier between
 //   warps).  Rows are XOR-swizzled in 16-byte chunks, so that ldmatrix (keys)
 //   and its transposing form (values: the halves of neighbouring tokens side
-//   by side) are free of bank conflicts.  q is the left operand (heads x
-//   dims), so scores land with heads in rows, which is the layout the second
-//   product wants p in: probabilities never leave registers.  mma.sync, not
-//   tcgen05: with at most 16 rows of q the product is a sixth of what the
-//   warp-level instruction can do, and the codes reach it from registers.
+//   by side) are free of bank conflicts.  Keys are the left operand (tokens x
+//   dims): a thread then holds 4 tokens x 2 heads of a tile and needs the
+//   scales of 4 tokens; with q on the left it would be 8 tokens, each read and
+//   unpacked by 8 lanes (the first form of this kernel took 119 us instead of
+//   88 us at 8 x 32K, 64/8 heads).  p s turns into the second product's layout
+//   with movmatrix.  mma.sync, not tcgen05: with at most 16 columns of q the
+//   product is a sixth of what the warp-level instruction can do, and the
+//   codes reach it from registers.
 //   A warp whose share ends inside a pair leaves its m, l and partial output.
 // finalize kernel: joins the partials of each pair (one CTA per q head), turns
 //   the stored scores into probabilities and adds them up over the group's
@@ -75,6 +78,7 @@ struct Decode4Params {
   // workspace
   int* status;
   int32_t* eff_len;     // [B] length after the append, -1: rejected
+  int32_t* tile_pre;    // [B + 1] tiles of one kv head before sequence b, and of all
   float2* part_ml;      // [warps + pairs][G]
   float* part_o;        // [warps + pairs][G][128]
   float scale, softcap;
@@ -180,11 +184,17 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       if (w < warp) base += s_scan[w];
       sum += s_scan[w];
     }
-    if (b < P.B) s_tiles[b] = base + x - n;
+    if (b < P.B) {
+      s_tiles[b] = base + x - n;
+      if (blockIdx.x == 0) P.tile_pre[b] = base + x - n;
+    }
     carry = sum;
     __syncthreads();
   }
-  if (tid == 0) s_tiles[P.B] = carry;
+  if (tid == 0) {
+    s_tiles[P.B] = carry;
+    if (blockIdx.x == 0) P.tile_pre[P.B] = carry;
+  }
   __syncthreads();
   const long long T = (long long)carry * P.Hkv;
   const long long N = min((long long)P.warps, T);
@@ -222,9 +232,10 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
     int pos_q = S - 1;
     if (kMod && mapped) pos_q = append ? __ldcg(P.next_pos + b) : __ldcg(prow + S - 1);
 
-    // q of this thread's head rows: fragments, group sums, power-of-two scale
+    // q: fragments of head g8 (+ 8), scaled by a power of two; group sums and factors of the heads
+    // 2 t4, 2 t4 + 1 (+ 8) whose scores this thread holds
     uint32_t qa[kH][4][4];   // per group: {dims 0,4}, {1,5}/16, {2,6}, {3,7}/16 of the thread's word
-    float qs[kH][4], mult[kH], slope[kH];
+    float qs[kH][4][2], mult[kH][2], slope[kH][2];
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       const int head = g8 + 8 * h;
@@ -244,6 +255,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       // largest magnitude in [2^(e-127), 2^(e-126)), e = top >> 23; q' = q 2^(14-(e-127))
       const int e = max(int(top >> 23), 15);
       const float up = __uint_as_float(uint32_t(268 - e) << 23);   // 13 <= 268 - e <= 253
+      float sums[4];
 #pragma unroll
       for (int gq = 0; gq < 4; ++gq) {
         const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
@@ -260,73 +272,107 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
         qa[h][gq][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[h][gq] = sum * 0x1p-24f;   // as if it had come out of the product with the codes
+        sums[gq] = sum * 0x1p-24f;   // as if it had come out of the product with the codes
       }
       // a product with the codes is 2^(141-e-24) times the true one
-      mult[h] = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
-      slope[h] = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
-      if (!kMod) mult[h] *= kLog2e;
-    }
-
-    float m[kH], l[kH], zacc[kH][4], o[kH][4][8];
-    int e_v[4];               // per group: 2^e_v is above every value scale so far
+      float f = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
+      const float sl = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
+      if (!kMod) f *= kLog2e;
 #pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
+      for (int k = 0; k < 2; ++k) {
+        const int from = 8 * t4 + 4 * k;   // a lane of head 2 t4 + k
 #pragma unroll
-      for (int gq = 0; gq < 4; ++gq) {
-        zacc[h][gq] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[h][gq][i] = 0.f;
+        for (int gq = 0; gq < 4; ++gq) qs[h][gq][k] = __shfl_sync(0xffffffffu, sums[gq], from);
+        mult[h][k] = __shfl_sync(0xffffffffu, f, from);
+        slope[h][k] = kMod ? __shfl_sync(0xffffffffu, sl, from) : 0.f;
       }
     }
+
+    float m[kH][2], l[kH][2], zacc[kH][4][2], o[kH][4][8];
+    int e_v[4];               // per group: 2^(e_v - 127) is above every value scale so far
+#pragma unroll
+    for (int h = 0; h < kH; ++h)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[h][k] = -INFINITY;
+        l[h][k] = 0.f;
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          zacc[h][gq][k] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[h][gq][4 * k + i] = 0.f;
+        }
+      }
 #pragma unroll
     for (int gq = 0; gq < 4; ++gq) e_v[gq] = 28;   // scales are 0 or at least 2^-100
 
-    // copies of tile i into its stage; bad pages and slots past S leave zeros
-    auto fetch = [&](int i) {
-      QdStage& st = ring[(i - i0) % kStages];
+    // Page-table entries of a tile's two 16-token halves, read a tile ahead of its copies; copies of
+    // tile i into its stage, zeros for bad pages and slots past S.
+    auto pages_of = [&](int i, int (&ph)[2]) {
+      if (i >= i1) return;
       const int s0 = ts.slot0(i);
-      const int r0 = lane >> 2, c = lane & 3;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int s1 = s0 + 16 * half;
-        int phys = -1;
-        if (s1 < S) phys = __ldg(bt + (s1 >> P.page_lg));
-        const bool ok = unsigned(phys) < unsigned(P.num_pages);
-        const long long base = ((((long long)(ok ? phys : 0) * P.Hkv + kvh)) << P.page_lg) + (s1 & page_mask);
+        ph[half] = s1 < S ? __ldg(bt + (s1 >> P.page_lg)) : -1;
+      }
+    };
+    const int c_dst = (lane >> 2) * kQ4CodeBytes + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    auto fetch = [&](int i, const int (&ph)[2]) {
+      QdStage& st = ring[(i - i0) % kStages];
+      const int s0 = ts.slot0(i);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const bool ok = unsigned(ph[half]) < unsigned(P.num_pages);
+        const size_t base = ((((size_t)(ok ? ph[half] : 0) * P.Hkv + kvh)) << P.page_lg) + ((s0 + 16 * half) & page_mask);
         const int bytes = ok ? 16 : 0;
+        const uint8_t* ck = P.codes[0] + base * kQ4CodeBytes + lane * 16;
+        const uint8_t* cv = P.codes[1] + base * kQ4CodeBytes + lane * 16;
+        const uint32_t dk = smem_u32(st.k) + half * 1024 + c_dst, dv = smem_u32(st.v) + half * 1024 + c_dst;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int r = 8 * k + r0, row = 16 * half + r;
-          const int off = row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4);
-          const size_t src = (size_t)(base + r) * kQ4CodeBytes + c * 16;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st.k + off)), "l"(P.codes[0] + src), "r"(bytes) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st.v + off)), "l"(P.codes[1] + src), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk + k * 512), "l"(ck + k * 512), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dv + k * 512), "l"(cv + k * 512), "r"(bytes) : "memory");
         }
-        const int r = lane & 15, side = lane >> 4;
-        const size_t src = (size_t)(base + r) * kQ4ScaleBytes;
-        uint4* dst = (side ? st.vs : st.ks) + 16 * half + r;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(P.scales[side] + src), "r"(bytes) : "memory");
+        const uint8_t* sc = P.scales[lane >> 4] + (base + (lane & 15)) * kQ4ScaleBytes;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32((lane >> 4 ? st.vs : st.ks) + 16 * half + (lane & 15))), "l"(sc), "r"(bytes) : "memory");
       }
       if (kMod && mapped) {
         const int s = s0 + lane;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(st.pos + lane)), "l"(prow + min(s, S - 1)), "r"(s < S ? 4 : 0) : "memory");
       }
     };
+    // ph_in: entries of the tiles already under way, by stage; ph_next: of the next one to fetch
+    int ph_in[kStages][2], ph_next[2] = {-1, -1};
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) ph_in[k][0] = ph_in[k][1] = -1;
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) {
-      if (i0 + k < i1) fetch(i0 + k);
+      if (i0 + k < i1) {
+        pages_of(i0 + k, ph_in[k]);
+        fetch(i0 + k, ph_in[k]);
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    pages_of(i0 + kStages - 1, ph_next);
 
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
+      const int ph0 = ph_in[0][0], ph1 = ph_in[0][1];
+#pragma unroll
+      for (int k = 0; k + 1 < kStages; ++k) {
+        ph_in[k][0] = ph_in[k + 1][0];
+        ph_in[k][1] = ph_in[k + 1][1];
+      }
       // the stage read last is free now: the next tile goes there
-      if (i + kStages - 1 < i1) fetch(i + kStages - 1);
+      if (i + kStages - 1 < i1) {
+        fetch(i + kStages - 1, ph_next);
+        ph_in[kStages - 2][0] = ph_next[0];
+        ph_in[kStages - 2][1] = ph_next[1];
+        pages_of(i + kStages, ph_next);
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
       QdStage& st = ring[(i - i0) % kStages];
       const int s0 = ts.slot0(i);
@@ -334,7 +380,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       // ---- the appended token: quantised here, into the pool and into this tile
       if (append && s0 <= S - 1 && S - 1 < s0 + kQdTile) {
         const int row = S - 1 - s0;
-        const int phys = __ldg(bt + ((S - 1) >> P.page_lg));
+        const int phys = row < 16 ? ph0 : ph1;
         if (unsigned(phys) < unsigned(P.num_pages)) {
           const long long prow_i = ((((long long)phys * P.Hkv + kvh)) << P.page_lg) + ((S - 1) & page_mask);
 #pragma unroll
@@ -364,9 +410,9 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       uint32_t vis;
       {
         const int s = s0 + lane;
-        bool see = s < S;
-        if (see) see = unsigned(__ldg(bt + (s >> P.page_lg))) < unsigned(P.num_pages);
-        if (s < S && !see) report(P.status, KVSEL_ERR_BAD_INDEX);
+        const bool live = s < S, paged = unsigned(lane < 16 ? ph0 : ph1) < unsigned(P.num_pages);
+        bool see = live && paged;
+        if (live && !paged) report(P.status, KVSEL_ERR_BAD_INDEX);
         if (kMod && P.window > 0) {
           const int p = mapped ? st.pos[lane] : s;
           see = see && (pos_q - p < P.window || p < P.n_sink);
@@ -382,7 +428,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
         const uint32_t sc[4] = {own.x & 0x7F80u, own.y & 0x7F80u, own.z & 0x7F80u, own.w & 0x7F80u};
         bool grow = false;
 #pragma unroll
-        for (int gq = 0; gq < 4; ++gq) grow |= int(sc[gq] >> 7) >= e_v[gq];
+        for (int gq = 0; gq < 4; ++gq) grow |= sc[gq] >= uint32_t(e_v[gq]) << 7;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int gq = 0; gq < 4; ++gq) {
@@ -400,91 +446,105 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
         }
         __syncwarp();
       }
+      const uint32_t vis_own = vis >> g8;   // bit 8 r: this thread's token 8 r + g8
 
-      // ---- scores: heads g8 (+ 8) x tokens 8 j + 2 t4, + 1
+      // ---- scores: tokens 8 r + g8 x heads 2 t4, 2 t4 + 1 (+ 8)
       float x[kH][4][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // words t4 of groups 0..3 of token 8 j + g8: matrix i of the load is group i
-        uint32_t w[4];
-        {
-          const int row = 8 * j + (lane & 7), c = lane >> 3;
-          ldsm_x4(smem_u32(st.k + row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4)), w[0], w[1], w[2], w[3]);
-        }
-        const uint4 sz0 = st.ks[8 * j + 2 * t4], sz1 = st.ks[8 * j + 2 * t4 + 1];
-        const uint32_t a0[4] = {sz0.x, sz0.y, sz0.z, sz0.w}, a1[4] = {sz1.x, sz1.y, sz1.z, sz1.w};
+      for (int mt = 0; mt < 2; ++mt) {
+        // words t4 of groups 0..3 of tokens 16 mt + g8 and + 8
+        uint32_t w[2][4];
+        uint4 sz[2];
 #pragma unroll
-        for (int h = 0; h < kH; ++h) x[h][j][0] = x[h][j][1] = 0.f;
+        for (int r = 0; r < 2; ++r) {
+          const int row = 16 * mt + 8 * r + (lane & 7), c = lane >> 3;
+          ldsm_x4(smem_u32(st.k + row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4)), w[r][0], w[r][1], w[r][2], w[r][3]);
+          sz[r] = st.ks[16 * mt + 8 * r + g8];
+        }
+        const uint32_t s0w[4] = {sz[0].x, sz[0].y, sz[0].z, sz[0].w}, s1w[4] = {sz[1].x, sz[1].y, sz[1].z, sz[1].w};
+#pragma unroll
+        for (int h = 0; h < kH; ++h) x[h][2 * mt][0] = x[h][2 * mt][1] = x[h][2 * mt + 1][0] = x[h][2 * mt + 1][1] = 0.f;
 #pragma unroll
         for (int gq = 0; gq < 4; ++gq) {
-          const uint32_t hi = w[gq] >> 8;
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16_16816(c, qa[0][gq][0], kWide ? qa[kH - 1][gq][0] : 0u, qa[0][gq][1], kWide ? qa[kH - 1][gq][1] : 0u,
-                        w[gq] & 0x000F000Fu, w[gq] & 0x00F000F0u);
-          mma_f16_16816(c, qa[0][gq][2], kWide ? qa[kH - 1][gq][2] : 0u, qa[0][gq][3], kWide ? qa[kH - 1][gq][3] : 0u,
-                        hi & 0x000F000Fu, hi & 0x00F000F0u);
+          const uint32_t u0 = w[0][gq] >> 8, u1 = w[1][gq] >> 8;
+          const uint32_t a[8] = {w[0][gq] & 0x000F000Fu, w[1][gq] & 0x000F000Fu, w[0][gq] & 0x00F000F0u, w[1][gq] & 0x00F000F0u,
+                                 u0 & 0x000F000Fu,       u1 & 0x000F000Fu,       u0 & 0x00F000F0u,       u1 & 0x00F000F0u};
+          const float sa = bf16lo_to_f32(s0w[gq]), za = bf16hi_to_f32(s0w[gq]);
+          const float sb = bf16lo_to_f32(s1w[gq]), zb = bf16hi_to_f32(s1w[gq]);
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            x[h][j][0] = fmaf(bf16lo_to_f32(a0[gq]), c[2 * h], fmaf(bf16hi_to_f32(a0[gq]), qs[h][gq], x[h][j][0]));
-            x[h][j][1] = fmaf(bf16lo_to_f32(a1[gq]), c[2 * h + 1], fmaf(bf16hi_to_f32(a1[gq]), qs[h][gq], x[h][j][1]));
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16_16816(c, a[0], a[1], a[2], a[3], qa[h][gq][0], qa[h][gq][1]);
+            mma_f16_16816(c, a[4], a[5], a[6], a[7], qa[h][gq][2], qa[h][gq][3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              x[h][2 * mt][k] = fmaf(sa, c[k], fmaf(za, qs[h][gq][k], x[h][2 * mt][k]));
+              x[h][2 * mt + 1][k] = fmaf(sb, c[2 + k], fmaf(zb, qs[h][gq][k], x[h][2 * mt + 1][k]));
+            }
           }
         }
       }
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float y = x[h][j][k] * mult[h];
+            float y = x[h][r][k] * mult[h][k];
             if (kMod) {
               if (P.softcap > 0.f) y = P.softcap * tanh_acc(__fdividef(y, P.softcap));
               y *= kLog2e;
               if (P.slopes) {
-                const int t = 8 * j + 2 * t4 + k;
+                const int t = 8 * r + g8;
                 const int p = mapped ? st.pos[t] : s0 + t;
-                y = fmaf(-slope[h], fabsf(float(pos_q - p)), y);
+                y = fmaf(-slope[h][k], fabsf(float(pos_q - p)), y);
               }
             }
-            x[h][j][k] = (vis >> (8 * j + 2 * t4 + k)) & 1u ? y : -INFINITY;
+            x[h][r][k] = (vis_own >> (8 * r)) & 1u ? y : -INFINITY;
           }
-        if (P.logits && g8 + 8 * h < P.G) {
-          float* lrow = P.logits + ((size_t)b * P.Hq + kvh * P.G + g8 + 8 * h) * P.max_len + s0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int t = 8 * j + 2 * t4 + k;
-              if (s0 + t < S) lrow[t] = x[h][j][k];
-            }
-        }
-        // running maximum and sum
-        float mx = m[h];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(x[h][j][0], x[h][j][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float use = mx == -INFINITY ? 0.f : mx;
-        if (__any_sync(0xffffffffu, mx > m[h])) {
-          const float corr = ex2(m[h] - use);
-          m[h] = mx;
-          l[h] *= corr;
-#pragma unroll
-          for (int gq = 0; gq < 4; ++gq) zacc[h][gq] *= corr;
-          // the output has heads in its columns 2 t4, 2 t4 + 1
-          const float c0 = __shfl_sync(0xffffffffu, corr, 8 * t4), c1 = __shfl_sync(0xffffffffu, corr, 8 * t4 + 4);
-#pragma unroll
-          for (int gq = 0; gq < 4; ++gq)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[h][gq][k] *= (k & 1) ? c1 : c0;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
+        if (P.logits) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            x[h][j][k] = ex2(x[h][j][k] - use);
-            l[h] += x[h][j][k];
+            const int head = 8 * h + 2 * t4 + k;
+            if (head < P.G) {
+              float* lrow = P.logits + ((size_t)b * P.Hq + kvh * P.G + head) * P.max_len + s0 + g8;
+              if (s0 + kQdTile <= S) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) lrow[8 * r] = x[h][r][k];
+              } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  if (s0 + 8 * r + g8 < S) lrow[8 * r] = x[h][r][k];
+              }
+            }
           }
+        }
+        // running maximum and sum
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float mx = fmaxf(fmaxf(x[h][0][k], x[h][1][k]), fmaxf(x[h][2][k], x[h][3][k]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx, m[h][k]);
+          const float use = mx == -INFINITY ? 0.f : mx;
+          if (__any_sync(0xffffffffu, mx > m[h][k])) {
+            const float corr = ex2(m[h][k] - use);
+            m[h][k] = mx;
+            l[h][k] *= corr;
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+              zacc[h][gq][k] *= corr;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) o[h][gq][2 * q + k] *= corr;   // columns are heads too
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[h][r][k] = ex2(x[h][r][k] - use);
+            l[h][k] += x[h][r][k];
+          }
+        }
       }
 
       // ---- output: (dims x tokens) codes times (tokens x heads) p s, per group
@@ -492,27 +552,29 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
 #pragma unroll
       for (int gq = 0; gq < 4; ++gq) inv_e[gq] = __uint_as_float(uint32_t(268 - e_v[gq]) << 23);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int mt = 0; mt < 2; ++mt) {
         uint32_t pb[kH][4][2];
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int j = 2 * half + jj;
-          const uint4 sz0 = st.vs[8 * j + 2 * t4], sz1 = st.vs[8 * j + 2 * t4 + 1];
-          const uint32_t a0[4] = {sz0.x, sz0.y, sz0.z, sz0.w}, a1[4] = {sz1.x, sz1.y, sz1.z, sz1.w};
+        for (int r = 0; r < 2; ++r) {
+          const uint4 sz = st.vs[16 * mt + 8 * r + g8];
+          const uint32_t sw[4] = {sz.x, sz.y, sz.z, sz.w};
 #pragma unroll
           for (int gq = 0; gq < 4; ++gq) {
-            const float f0 = bf16lo_to_f32(a0[gq]) * inv_e[gq], f1 = bf16lo_to_f32(a1[gq]) * inv_e[gq];
+            const float f = bf16lo_to_f32(sw[gq]) * inv_e[gq], z = bf16hi_to_f32(sw[gq]);
 #pragma unroll
             for (int h = 0; h < kH; ++h) {
-              pb[h][gq][jj] = pack_f16x2(x[h][j][0] * f0, x[h][j][1] * f1);
-              zacc[h][gq] = fmaf(x[h][j][0], bf16hi_to_f32(a0[gq]), fmaf(x[h][j][1], bf16hi_to_f32(a1[gq]), zacc[h][gq]));
+              const float p0 = x[h][2 * mt + r][0], p1 = x[h][2 * mt + r][1];
+              // token g8 x heads 2 t4, + 1 -> tokens 2 t4, + 1 of head g8
+              asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pb[h][gq][r]) : "r"(pack_f16x2(p0 * f, p1 * f)));
+              zacc[h][gq][0] = fmaf(p0, z, zacc[h][gq][0]);
+              zacc[h][gq][1] = fmaf(p1, z, zacc[h][gq][1]);
             }
           }
         }
         // halves g8 of groups 0..3, tokens 2 t4 and 2 t4 + 1 of the 8 (lo) and the next 8 (hi)
         uint32_t lo[4], hi[4];
         {
-          const int row = 16 * half + (lane & 7), c = lane >> 3;
+          const int row = 16 * mt + (lane & 7), c = lane >> 3;
           const int off = ((c ^ ((row >> 1) & 3)) << 4);
           ldsm_x4_t(smem_u32(st.v + row * kQ4CodeBytes + off), lo[0], lo[1], lo[2], lo[3]);
           ldsm_x4_t(smem_u32(st.v + (row + 8) * kQ4CodeBytes + off), hi[0], hi[1], hi[2], hi[3]);
@@ -540,29 +602,37 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
     const long long slot = wid + rowi;   // the staircase of (warp, pair) visits each sum once
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
-      float lsum = l[h];
-      lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-      lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-      if (t4 == 0 && g8 + 8 * h < P.G) P.part_ml[slot * P.G + g8 + 8 * h] = make_float2(m[h], lsum);
+      const int head = 8 * h + 2 * t4;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float lsum = l[h][k];
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 4);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+        if (g8 == 0 && head + k < P.G) P.part_ml[slot * P.G + head + k] = make_float2(m[h][k], lsum);
+      }
 #pragma unroll
       for (int gq = 0; gq < 4; ++gq) {
-        float z = zacc[h][gq];
-        z += __shfl_xor_sync(0xffffffffu, z, 1);
-        z += __shfl_xor_sync(0xffffffffu, z, 2);
-        const float z0 = __shfl_sync(0xffffffffu, z, 8 * t4), z1 = __shfl_sync(0xffffffffu, z, 8 * t4 + 4);
+        float z[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          z[k] = zacc[h][gq][k];
+          z[k] += __shfl_xor_sync(0xffffffffu, z[k], 4);
+          z[k] += __shfl_xor_sync(0xffffffffu, z[k], 8);
+          z[k] += __shfl_xor_sync(0xffffffffu, z[k], 16);
+        }
         // codes were n 2^-24 (dims 0, 2) and n 2^-20 (dims 1, 3), p s was p s 2^(141 - e): undone in
         // two factors so that neither overflows
         const float back = __uint_as_float(uint32_t(e_v[gq] - 14) << 23);
         const float* a = o[h][gq];
         const float c24 = 0x1p24f, c20 = 0x1p20f;
-        const float4 r0 = make_float4(fmaf(a[0] * c24, back, z0), fmaf(a[2] * c20, back, z0),
-                                      fmaf(a[4] * c24, back, z0), fmaf(a[6] * c20, back, z0));
-        const float4 r1 = make_float4(fmaf(a[1] * c24, back, z1), fmaf(a[3] * c20, back, z1),
-                                      fmaf(a[5] * c24, back, z1), fmaf(a[7] * c20, back, z1));
-        const int head = 8 * h + 2 * t4;
         float* po = P.part_o + (slot * P.G + head) * kQ4D + 32 * gq + 4 * g8;
-        if (head < P.G) *reinterpret_cast<float4*>(po) = r0;
-        if (head + 1 < P.G) *reinterpret_cast<float4*>(po + kQ4D) = r1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (head + k < P.G)
+            *reinterpret_cast<float4*>(po + k * kQ4D) =
+                make_float4(fmaf(a[k] * c24, back, z[k]), fmaf(a[2 + k] * c20, back, z[k]),
+                            fmaf(a[4 + k] * c24, back, z[k]), fmaf(a[6 + k] * c20, back, z[k]));
       }
     }
     tile += i1 - i0;
@@ -575,7 +645,6 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
   __shared__ float s_m[16], s_inv[16];
   __shared__ float s_red[kQfThreads / 32];
   __shared__ float s_o[kQfThreads / 32][kQ4D];
-  __shared__ int s_pre[kQfThreads / 32], s_tot[kQfThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kvh = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -589,27 +658,7 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
   }
   if (chunk >= 0 && chunk * kQfSlots >= S) return;
 
-  // tiles before this sequence, and of all
-  int pre = 0, tot = 0;
-  for (int i = tid; i < P.B; i += kQfThreads) {
-    const int Si = __ldcg(P.eff_len + i);
-    const int n = Si > 0 ? tiles_of(Si, P.window, P.n_sink, mapped).count : 0;
-    tot += n;
-    if (i < b) pre += n;
-  }
-  pre = __reduce_add_sync(0xffffffffu, pre);
-  tot = __reduce_add_sync(0xffffffffu, tot);
-  if (lane == 0) {
-    s_pre[warp] = pre;
-    s_tot[warp] = tot;
-  }
-  __syncthreads();
-  pre = tot = 0;
-#pragma unroll
-  for (int w = 0; w < kQfThreads / 32; ++w) {
-    pre += s_pre[w];
-    tot += s_tot[w];
-  }
+  const int pre = __ldcg(P.tile_pre + b), tot = __ldcg(P.tile_pre + P.B);
   const TileSet ts = tiles_of(S, P.window, P.n_sink, mapped);
   const long long T = (long long)tot * P.Hkv, N = min((long long)P.warps, T);
   const long long t0 = (long long)pre * P.Hkv + (long long)kvh * ts.count;
@@ -663,20 +712,29 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     return;
   }
 
-  // every head's maximum and 1 / sum: 16 threads a head
+  // every head's maximum and 1 / sum: 16 threads a head, the first 4 partials of each read at once
   {
     const int head = tid >> 4, l16 = tid & 15;
-    float mx = -INFINITY;
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = l16 + 16 * k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (head < P.G && i < n_part) ml[k] = __ldcg(&P.part_ml[(first + i) * P.G + head]);
+    }
+    float mx = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
     if (head < P.G)
-      for (int i = l16; i < n_part; i += 16) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
+      for (int i = l16 + 64; i < n_part; i += 16) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
 #pragma unroll
     for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float use = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum = fmaf(ml[k].y, ex2(ml[k].x - use), sum);
     if (head < P.G)
-      for (int i = l16; i < n_part; i += 16) {
-        const float2 ml = __ldcg(&P.part_ml[(first + i) * P.G + head]);
-        sum = fmaf(ml.y, ex2(ml.x - use), sum);
+      for (int i = l16 + 64; i < n_part; i += 16) {
+        const float2 v = __ldcg(&P.part_ml[(first + i) * P.G + head]);
+        sum = fmaf(v.y, ex2(v.x - use), sum);
       }
 #pragma unroll
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -689,19 +747,39 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
   const float* lg = P.logits + ((size_t)b * P.Hq + kvh * P.G) * P.max_len;
   float* crow = P.cum ? P.cum + rowi * P.max_len : nullptr;
   const int new_slot = P.new_kv[0] ? S - 1 : -1;
+  constexpr int kPer = kQfSlots / kQfThreads;
+  const int s0 = chunk * kQfSlots + tid;
+  bool use[kPer];
+  float sum[kPer], old[kPer];
 #pragma unroll
-  for (int k = 0; k < kQfSlots / kQfThreads; ++k) {
-    const int s = chunk * kQfSlots + k * kQfThreads + tid;
-    if (s >= S) break;
-    const bool visited = ts.holds(s / kQdTile);
-    float sum = 0.f;
-#pragma unroll 8
-    for (int h = 0; h < P.G; ++h) {
-      const float p = visited ? ex2(__ldcg(lg + (size_t)h * P.max_len + s) - s_m[h]) * s_inv[h] : 0.f;
-      if (P.probs) P.probs[((size_t)b * P.Hq + kvh * P.G + h) * P.max_len + s] = p;
-      sum += p;
+  for (int k = 0; k < kPer; ++k) {
+    const int s = s0 + k * kQfThreads;
+    use[k] = s < S && ts.holds(s / kQdTile);
+    sum[k] = 0.f;
+    old[k] = crow && use[k] && s != new_slot ? __ldcg(crow + s) : 0.f;   // the appended slot starts from 0
+  }
+#pragma unroll 4
+  for (int h = 0; h < P.G; ++h) {
+    float v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) v[k] = use[k] ? __ldcs(lg + (size_t)h * P.max_len + s0 + k * kQfThreads) : -INFINITY;
+    const float mh = s_m[h], ih = s_inv[h];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      v[k] = ex2(v[k] - mh) * ih;
+      sum[k] += v[k];
     }
-    if (crow && (visited || s == new_slot)) crow[s] = s == new_slot ? sum : crow[s] + sum;
+    if (P.probs) {
+      float* pr = P.probs + ((size_t)b * P.Hq + kvh * P.G + h) * P.max_len + s0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (s0 + k * kQfThreads < S) pr[k * kQfThreads] = v[k];
+    }
+  }
+  if (crow) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (use[k]) crow[s0 + k * kQfThreads] = old[k] + sum[k];
   }
 }
 
@@ -715,7 +793,7 @@ namespace {
 constexpr int kQdStages = 2;
 
 struct Decode4Ws {
-  size_t eff_off, ml_off, o_off, logits_off, total;
+  size_t eff_off, pre_off, ml_off, o_off, logits_off, total;
 };
 
 // CTAs of the main kernel: every co-resident slot (8 warps each; two CTAs an
@@ -729,7 +807,8 @@ Decode4Ws decode4_layout(const kvsel_paged_kv4* kv, int batch, int max_len, bool
   const size_t parts = size_t(ctas) * kQdWarps + size_t(batch) * kv->num_kv_heads;
   Decode4Ws w;
   w.eff_off = kStatusBytes;
-  w.ml_off = align_up(w.eff_off + size_t(batch) * 4, 256);
+  w.pre_off = align_up(w.eff_off + size_t(batch) * 4, 256);
+  w.ml_off = align_up(w.pre_off + size_t(batch + 1) * 4, 256);
   w.o_off = align_up(w.ml_off + parts * G * sizeof(float2), 256);
   w.logits_off = align_up(w.o_off + parts * G * kQ4D * sizeof(float), 256);
   w.total = w.logits_off + (own_logits ? align_up(size_t(batch) * kv->num_q_heads * max_len * sizeof(float), 256) : 0);
@@ -819,6 +898,7 @@ extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const i
   P.cum = h2o_cum;
   P.status = reinterpret_cast<int*>(ws);
   P.eff_len = reinterpret_cast<int32_t*>(ws + L.eff_off);
+  P.tile_pre = reinterpret_cast<int32_t*>(ws + L.pre_off);
   P.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   P.part_o = reinterpret_cast<float*>(ws + L.o_off);
   P.scale = scale;

@@ -700,7 +700,8 @@ typedef struct kvsel_paged_kv4 {
  *   seq_lens     int32 [batch], in/out: grows by each sequence's run.
  *   tok_off      int32 [batch + 1] (device), non-decreasing from 0 on, at most
  *                total_tokens; packed rows past tok_off[batch] are ignored.
- *   k, v         bf16 [total_tokens][num_kv_heads][128].
+ *   k, v         bf16 [total_tokens][num_kv_heads][128]; total_tokens *
+ *                num_kv_heads < 2^31 - 2^20 (else UNSUPPORTED), here and below.
  *   pos_map      int32 [batch][num_kv_heads][max_len] or NULL: the new slots get
  *                next_pos[b], next_pos[b] + 1, ...
  *   next_pos     int32 [batch] or NULL (required with pos_map): grows with seq_lens.
