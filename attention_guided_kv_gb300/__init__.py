@@ -559,10 +559,57 @@ def _shaped(t, shape, name):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}")
+def _arg(t, dtype, shape, dev, name):
+    """Data pointer of a tensor after its checks (None for an argument that is not given)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, dtype, name)
+    _shaped(t, shape, name)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _required(t, dtype, shape, dev, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _arg(t, dtype, shape, dev, name)
+
+
+def _scratch(workspace, dev):
+    """(pointer, bytes) of a workspace of any type."""
+    return _required(workspace, workspace.dtype, workspace.shape, dev, "workspace"), workspace.nbytes
+
+
+def _output(out, shape, dev):
+    """(pointer, dtype code) of an output in bf16 or fp32."""
+    if out.dtype is torch.float32:
+        return _required(out, torch.float32, shape, dev, "out"), KVSEL_F32
+    if out.dtype is not torch.bfloat16:
+        raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor")
+    return _required(out, torch.bfloat16, shape, dev, "out"), KVSEL_BF16
+
+
+class _On:
+    """Enters a tensor's device where it is not the current one (the library launches on the current device)."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, dev):
+        self.ctx = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _queue(stream, dev):
+    """Handle of the given stream, or of the device's current one."""
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
 def paged_kv4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
@@ -579,84 +626,70 @@ def paged_kv4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tens
     _shaped(v_codes, k_codes.shape, "v_codes")
     _shaped(k_scales, (P, H, pg, half // 16, 2), "k_scales")
     _shaped(v_scales, (P, H, pg, half // 16, 2), "v_scales")
-    _same_device(k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
+    for t, name in ((v_codes, "v_codes"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.device != k_codes.device:
+            raise ValueError(f"{name} must be on {k_codes.device}")
     return PagedKV4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), P, H, num_q_heads,
                     2 * half, pg)
 
 
 def _table_of(block_table, seq_lens):
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
-    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError("block_table must be [batch][max_pages] and seq_lens [batch]")
-    return seq_lens.shape[0]
+    """(batch, max_pages, device, pointers) of a block table and its lengths."""
+    if block_table is None or block_table.dim() != 2 or block_table.device.type != "cuda":
+        raise ValueError("block_table must be a CUDA tensor [batch][max_pages]")
+    dev = block_table.device
+    batch, pages = block_table.shape
+    return (batch, pages, dev, _arg(block_table, torch.int32, block_table.shape, dev, "block_table"),
+            _required(seq_lens, torch.int32, (batch,), dev, "seq_lens"))
 
 
-def _nbytes(t):
-    return t.numel() * t.element_size()
-
-
-def _per_slot(kv, batch, max_len, **tensors):
-    """The common row length of the given [batch][num_kv_heads][max_len] tensors (0 without any)."""
-    for name, t in tensors.items():
-        if t is not None:
-            max_len = t.shape[-1] if max_len is None else max_len
-            _shaped(t, (batch, kv.num_kv_heads, max_len), name)
+def _row_len(max_len, *tensors):
+    """max_len if it is given, else the row length of the first tensor that is."""
+    if max_len is None:
+        for t in tensors:
+            if t is not None:
+                return t.shape[-1]
     return max_len
 
 
 def kvsel_kv4_append_workspace(kv: PagedKV4, batch: int) -> int:
-    return int(lib().kvsel_kv4_append_workspace(ctypes.byref(kv), int(batch)))
+    return int(lib().kvsel_kv4_append_workspace(kv, int(batch)))
 
 
 def kvsel_kv4_append(kv: PagedKV4, block_table, seq_lens, tok_off, k, v, workspace, *, pos_map=None, next_pos=None,
                      h2o_cum=None, stream=None):
     """Quantise packed new tokens (k, v bf16 [total][Hkv][128]; sequence b's are rows tok_off[b]..tok_off[b + 1])
     into the cache behind each sequence's live ones; seq_lens (and next_pos) grow."""
-    batch = _table_of(block_table, seq_lens)
-    _need(tok_off, torch.int32, "tok_off")
-    _shaped(tok_off, (batch + 1,), "tok_off")
-    _need(k, torch.bfloat16, "k")
-    _need(v, torch.bfloat16, "v")
-    _shaped(k, (k.shape[0], kv.num_kv_heads, kv.head_dim), "k")
-    _shaped(v, k.shape, "v")
-    _need(pos_map, torch.int32, "pos_map", True)
-    _need(next_pos, torch.int32, "next_pos", True)
-    _shaped(next_pos, (batch,), "next_pos")
-    _need(h2o_cum, torch.float32, "h2o_cum", True)
-    _need(workspace, workspace.dtype, "workspace")
-    max_len = _per_slot(kv, batch, None, pos_map=pos_map, h2o_cum=h2o_cum) or 0
-    _same_device(block_table, seq_lens=seq_lens, tok_off=tok_off, k=k, v=v, pos_map=pos_map, next_pos=next_pos,
-                 h2o_cum=h2o_cum, workspace=workspace)
-    with torch.cuda.device(block_table.device):
+    batch, pages, dev, table, lens = _table_of(block_table, seq_lens)
+    total, heads = k.shape[0], kv.num_kv_heads
+    rows = (total, heads, kv.head_dim)
+    max_len = _row_len(None, pos_map, h2o_cum) or 0
+    ws, ws_bytes = _scratch(workspace, dev)
+    with _On(dev):
         _check(lib().kvsel_kv4_append(
-            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(tok_off), k.shape[0],
-            _ptr(k), _ptr(v), _ptr(pos_map), _ptr(next_pos), _ptr(h2o_cum), max_len, _ptr(workspace), _nbytes(workspace),
-            _stream(stream)))
+            kv, table, pages, lens, batch, _required(tok_off, torch.int32, (batch + 1,), dev, "tok_off"), total,
+            _required(k, torch.bfloat16, rows, dev, "k"), _required(v, torch.bfloat16, rows, dev, "v"),
+            _arg(pos_map, torch.int32, (batch, heads, max_len), dev, "pos_map"),
+            _arg(next_pos, torch.int32, (batch,), dev, "next_pos"),
+            _arg(h2o_cum, torch.float32, (batch, heads, max_len), dev, "h2o_cum"), max_len, ws, ws_bytes,
+            _queue(stream, dev)))
 
 
 def kvsel_kv4_read(kv: PagedKV4, block_table, seq_lens, tok_off, k_out, v_out, workspace, *, start=None, stream=None):
     """Read cached tokens back as bf16: packed row tok_off[b] + i is slot start[b] + i (or i) of sequence b."""
-    batch = _table_of(block_table, seq_lens)
-    _need(tok_off, torch.int32, "tok_off")
-    _shaped(tok_off, (batch + 1,), "tok_off")
-    _need(start, torch.int32, "start", True)
-    _shaped(start, (batch,), "start")
-    _need(k_out, torch.bfloat16, "k_out")
-    _need(v_out, torch.bfloat16, "v_out")
-    _shaped(k_out, (k_out.shape[0], kv.num_kv_heads, kv.head_dim), "k_out")
-    _shaped(v_out, k_out.shape, "v_out")
-    _need(workspace, workspace.dtype, "workspace")
-    _same_device(block_table, seq_lens=seq_lens, tok_off=tok_off, start=start, k_out=k_out, v_out=v_out,
-                 workspace=workspace)
-    with torch.cuda.device(block_table.device):
+    batch, pages, dev, table, lens = _table_of(block_table, seq_lens)
+    total = k_out.shape[0]
+    rows = (total, kv.num_kv_heads, kv.head_dim)
+    ws, ws_bytes = _scratch(workspace, dev)
+    with _On(dev):
         _check(lib().kvsel_kv4_read(
-            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(tok_off),
-            k_out.shape[0], _ptr(start), _ptr(k_out), _ptr(v_out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+            kv, table, pages, lens, batch, _required(tok_off, torch.int32, (batch + 1,), dev, "tok_off"), total,
+            _arg(start, torch.int32, (batch,), dev, "start"), _required(k_out, torch.bfloat16, rows, dev, "k_out"),
+            _required(v_out, torch.bfloat16, rows, dev, "v_out"), ws, ws_bytes, _queue(stream, dev)))
 
 
 def kvsel_kv4_decode_attn_workspace(kv: PagedKV4, batch: int, max_len: int, with_probs: bool, with_cum: bool) -> int:
-    return int(lib().kvsel_kv4_decode_attn_workspace(ctypes.byref(kv), int(batch), int(max_len), int(bool(with_probs)),
+    return int(lib().kvsel_kv4_decode_attn_workspace(kv, int(batch), int(max_len), int(bool(with_probs)),
                                                      int(bool(with_cum))))
 
 
@@ -669,73 +702,52 @@ def kvsel_kv4_decode_attn(kv: PagedKV4, block_table, seq_lens, q, out, workspace
     distance is taken off the score.  window: only the last `window` positions and the first `n_sink` are seen.
     Positions are pos_map's where it is given, else the slots.
     """
-    batch = _table_of(block_table, seq_lens)
-    _need(q, torch.bfloat16, "q")
-    _shaped(q, (batch, kv.num_q_heads, kv.head_dim), "q")
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _need(t, torch.bfloat16, name, True)
-        _shaped(t, (batch, kv.num_kv_heads, kv.head_dim), name)
-    _need(pos_map, torch.int32, "pos_map", True)
-    _need(next_pos, torch.int32, "next_pos", True)
-    _shaped(next_pos, (batch,), "next_pos")
-    _need(slopes, torch.float32, "slopes", True)
-    _shaped(slopes, (kv.num_q_heads,), "slopes")
-    _need(probs, torch.float32, "probs", True)
-    _need(h2o_cum, torch.float32, "h2o_cum", True)
-    _need(workspace, workspace.dtype, "workspace")
-    if out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous() or out.device.type != "cuda":
-        raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor")
-    _shaped(out, q.shape, "out")
-    if max_len is None and probs is not None:
-        max_len = probs.shape[-1]
-    max_len = _per_slot(kv, batch, max_len, pos_map=pos_map, h2o_cum=h2o_cum)
+    batch, pages, dev, table, lens = _table_of(block_table, seq_lens)
+    heads, kv_heads, bf16 = kv.num_q_heads, kv.num_kv_heads, torch.bfloat16
+    max_len = _row_len(max_len, probs, pos_map, h2o_cum)
     if max_len is None:
-        max_len = block_table.shape[1] * kv.page_size
-    _shaped(probs, (batch, kv.num_q_heads, max_len), "probs")
-    _same_device(block_table, seq_lens=seq_lens, q=q, out=out, k_new=k_new, v_new=v_new, pos_map=pos_map,
-                 next_pos=next_pos, slopes=slopes, probs=probs, h2o_cum=h2o_cum, workspace=workspace)
+        max_len = pages * kv.page_size
+    new, rows = (batch, kv_heads, kv.head_dim), (batch, kv_heads, max_len)
+    out_ptr, out_type = _output(out, (batch, heads, kv.head_dim), dev)
+    ws, ws_bytes = _scratch(workspace, dev)
     mod = None
     if softcap != 0 or slopes is not None or window != 0 or n_sink != 0:
-        mod = ScoreMod(float(softcap), slopes.data_ptr() if slopes is not None else None, int(window), int(n_sink))
-    with torch.cuda.device(block_table.device):
+        mod = ScoreMod(softcap, _arg(slopes, torch.float32, (heads,), dev, "slopes"), window, n_sink)
+    with _On(dev):
         _check(lib().kvsel_kv4_decode_attn(
-            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(q), _ptr(k_new),
-            _ptr(v_new), _ptr(pos_map), _ptr(next_pos), float(kv.head_dim ** -0.5 if scale is None else scale),
-            ctypes.byref(mod) if mod is not None else None, _ptr(out),
-            KVSEL_F32 if out.dtype == torch.float32 else KVSEL_BF16, _ptr(probs), _ptr(h2o_cum), int(max_len),
-            _ptr(workspace), _nbytes(workspace), _stream(stream)))
+            kv, table, pages, lens, batch, _required(q, bf16, (batch, heads, kv.head_dim), dev, "q"),
+            _arg(k_new, bf16, new, dev, "k_new"), _arg(v_new, bf16, new, dev, "v_new"),
+            _arg(pos_map, torch.int32, rows, dev, "pos_map"), _arg(next_pos, torch.int32, (batch,), dev, "next_pos"),
+            kv.head_dim ** -0.5 if scale is None else scale, mod, out_ptr, out_type,
+            _arg(probs, torch.float32, (batch, heads, max_len), dev, "probs"),
+            _arg(h2o_cum, torch.float32, rows, dev, "h2o_cum"), max_len, ws, ws_bytes, _queue(stream, dev)))
 
 
 def kvsel_kv4_evict_workspace(kv: PagedKV4, batch: int, budget: int) -> int:
-    return int(lib().kvsel_kv4_evict_workspace(ctypes.byref(kv), int(batch), int(budget)))
+    return int(lib().kvsel_kv4_evict_workspace(kv, int(batch), int(budget)))
 
 
 def kvsel_kv4_evict(kv: PagedKV4, block_table, seq_lens, h2o_cum, workspace, *, budget, n_sink, window, compact=False,
                     pos_map=None, keep_out=None, freed_pages=None, stream=None):
     """kvsel_h2o_evict for the 4-bit cache: select by accumulated weight; optional in-place compaction."""
-    batch = _table_of(block_table, seq_lens)
-    _need(h2o_cum, torch.float32, "h2o_cum")
-    _need(pos_map, torch.int32, "pos_map", True)
-    _need(keep_out, torch.int32, "keep_out", True)
-    _shaped(keep_out, (batch, kv.num_kv_heads, int(budget)), "keep_out")
-    _need(freed_pages, torch.int32, "freed_pages", True)
-    _shaped(freed_pages, block_table.shape, "freed_pages")
-    _need(workspace, workspace.dtype, "workspace")
-    max_len = _per_slot(kv, batch, None, h2o_cum=h2o_cum, pos_map=pos_map)
-    _same_device(block_table, seq_lens=seq_lens, h2o_cum=h2o_cum, pos_map=pos_map, keep_out=keep_out,
-                 freed_pages=freed_pages, workspace=workspace)
-    with torch.cuda.device(block_table.device):
+    batch, pages, dev, table, lens = _table_of(block_table, seq_lens)
+    heads, budget = kv.num_kv_heads, int(budget)
+    max_len = _row_len(None, h2o_cum, pos_map)
+    rows = (batch, heads, max_len)
+    ws, ws_bytes = _scratch(workspace, dev)
+    with _On(dev):
         _check(lib().kvsel_kv4_evict(
-            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(h2o_cum), _ptr(pos_map),
-            max_len, int(budget), int(n_sink), int(window), int(bool(compact)), _ptr(keep_out), _ptr(freed_pages),
-            _ptr(workspace), _nbytes(workspace), _stream(stream)))
+            kv, table, pages, lens, batch, _required(h2o_cum, torch.float32, rows, dev, "h2o_cum"),
+            _arg(pos_map, torch.int32, rows, dev, "pos_map"), max_len, budget, int(n_sink), int(window),
+            int(bool(compact)), _arg(keep_out, torch.int32, (batch, heads, budget), dev, "keep_out"),
+            _arg(freed_pages, torch.int32, (batch, pages), dev, "freed_pages"), ws, ws_bytes, _queue(stream, dev)))
 
 
 # ----------------------------------------------------------------------------
 # attention of prompt tokens
 # ----------------------------------------------------------------------------
 def kvsel_prefill_attn_workspace(kv: PagedKV, batch: int, total_q: int) -> int:
-    return int(lib().kvsel_prefill_attn_workspace(ctypes.byref(kv), int(batch), int(total_q)))
+    return int(lib().kvsel_prefill_attn_workspace(kv, int(batch), int(total_q)))
 
 
 def kvsel_prefill_attn(kv: PagedKV, block_table, seq_lens, q, q_off, out, workspace, *, scale=None, softcap=0.0,
@@ -748,29 +760,16 @@ def kvsel_prefill_attn(kv: PagedKV, block_table, seq_lens, q, q_off, out, worksp
     [batch]): positions that every query of the sequence sees.  doc_start (int32 [total]): the first position each
     query may see.  lse (fp32 [total][Hq]): log-sum-exp of each row's scores, -inf for a row that sees nothing.
     """
-    batch = _table_of(block_table, seq_lens)
-    _need(q, torch.bfloat16, "q")
-    _shaped(q, (q.shape[0], kv.num_q_heads, kv.head_dim), "q")
-    total = q.shape[0]
-    _need(q_off, torch.int32, "q_off")
-    _shaped(q_off, (batch + 1,), "q_off")
-    if out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous() or out.device.type != "cuda":
-        raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor")
-    _shaped(out, q.shape, "out")
-    _need(slopes, torch.float32, "slopes", True)
-    _shaped(slopes, (kv.num_q_heads,), "slopes")
-    _need(prefix, torch.int32, "prefix", True)
-    _shaped(prefix, (batch,), "prefix")
-    _need(doc_start, torch.int32, "doc_start", True)
-    _shaped(doc_start, (total,), "doc_start")
-    _need(lse, torch.float32, "lse", True)
-    _shaped(lse, q.shape[:2], "lse")
-    _need(workspace, workspace.dtype, "workspace")
-    _same_device(block_table, seq_lens=seq_lens, q=q, q_off=q_off, out=out, slopes=slopes, prefix=prefix,
-                 doc_start=doc_start, lse=lse, workspace=workspace)
-    with torch.cuda.device(block_table.device):
+    batch, pages, dev, table, lens = _table_of(block_table, seq_lens)
+    total, heads = q.shape[0], kv.num_q_heads
+    rows = (total, heads, kv.head_dim)
+    out_ptr, out_type = _output(out, rows, dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    with _On(dev):
         _check(lib().kvsel_prefill_attn(
-            ctypes.byref(kv), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), batch, _ptr(q), _ptr(q_off), total,
-            float(kv.head_dim ** -0.5 if scale is None else scale), float(softcap), _ptr(slopes), int(window),
-            _ptr(prefix), _ptr(doc_start), _ptr(out), KVSEL_F32 if out.dtype == torch.float32 else KVSEL_BF16, _ptr(lse),
-            _ptr(workspace), _nbytes(workspace), _stream(stream)))
+            kv, table, pages, lens, batch, _required(q, torch.bfloat16, rows, dev, "q"),
+            _required(q_off, torch.int32, (batch + 1,), dev, "q_off"), total,
+            kv.head_dim ** -0.5 if scale is None else scale, softcap,
+            _arg(slopes, torch.float32, (heads,), dev, "slopes"), int(window),
+            _arg(prefix, torch.int32, (batch,), dev, "prefix"), _arg(doc_start, torch.int32, (total,), dev, "doc_start"),
+            out_ptr, out_type, _arg(lse, torch.float32, (total, heads), dev, "lse"), ws, ws_bytes, _queue(stream, dev)))

@@ -49,19 +49,36 @@ __device__ __forceinline__ uint32_t q4_scale_bits(float hi_v, float lo_v) {
   return u < (27u << 7) ? 0u : u;       // 2^-100 has exponent field 27
 }
 
-// The code of x >= z in a group of minimum z and scale s > 0 (inv ~ 1 / s), as
-// a float.  Adding 1.5 * 2^23 rounds to an integer, ties to even.  No clamp:
-// s is at least (1 - 2^-8) / 15 of the range, so the quotient is below 15.1.
-__device__ __forceinline__ float q4_code(float x, float z, float s, float half_s, float inv) {
-  constexpr float kMagic = 12582912.f;
-  const float r = __fsub_rn(x, z);
-  float n = __fsub_rn(__fmaf_rn(r, inv, kMagic), kMagic);
+// Packed bf16 minimum and maximum (a NaN wins), and the smaller magnitude (of
+// either sign).
+__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_min_abs(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t swap_halves(uint32_t v) { return __funnelshift_l(v, v, 16); }
+
+// The code of x >= z in a group of minimum z and scale s, whatever the
+// magnitudes: x - z may need more than 24 bits, so its rounding error decides
+// where the quotient looks like a border.
+__device__ __forceinline__ float q4_code_any(float x, float z, float s, float inv) {
+  float err;
+  const float r = two_sum(x, -z, err);
+  float n = rintf(r * inv);
   const float d = __fmaf_rn(-n, s, r);
-  if (fabsf(d) >= half_s) {             // on or past a border: settle it exactly
-    float err;
-    const float rr = two_sum(x, -z, err);
+  if (fabsf(d) >= 0.5f * s) {
     const float f = d > 0.0f ? n : n - 1.0f;
-    const float e = __fadd_rn(__fsub_rn(rr, (f + 0.5f) * s), err);
+    const float e = __fadd_rn(__fsub_rn(r, (f + 0.5f) * s), err);
     const bool up = e > 0.0f || (e == 0.0f && (int(f) & 1));
     n = up ? f + 1.0f : f;
   }
@@ -70,48 +87,75 @@ __device__ __forceinline__ float q4_code(float x, float z, float s, float half_s
 
 // One group spread over 32 / NV neighbouring lanes of NV values each (bf16
 // pairs in raw): returns this lane's NV codes (4 bits each, value 0 lowest)
-// and the group's {s, z} bits.  All the group's lanes take part.
+// and the group's {s, z} bits.  All lanes of the warp take part.
+//
+// The usual case (no value below 2^-15 of the largest magnitude) has x - z
+// exact in fp32.  r / s is rounded by adding 1.5 * 2^23 to r * inv in one fused
+// step, with inv slightly above 1 / s: the result is the right code or one too
+// high, a tie always the upper one.  The exact remainder d = r - n s tells: it
+// is below -s/2, or equal to it at an odd n, where n is one too high; both in
+// one comparison with a threshold that is the next float below -s/2 for even n.
+// s is at least (1 - 2^-8) / 15 of the range, so n is at most 15.
 template <int NV>
 __device__ __forceinline__ uint32_t q4_group(const uint32_t (&raw)[NV / 2], uint32_t& sz) {
-  float x[NV];
-  uint32_t mag = 0;
+  uint32_t lo2 = raw[0], hi2 = raw[0], ab2 = raw[0];
 #pragma unroll
-  for (int i = 0; i < NV / 2; ++i) {
-    x[2 * i] = bf16lo_to_f32(raw[i]);
-    x[2 * i + 1] = bf16hi_to_f32(raw[i]);
-    mag = max(mag, max((raw[i] << 16) & 0x7FFF0000u, raw[i] & 0x7FFF0000u));
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < NV; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
+  for (int i = 1; i < NV / 2; ++i) {
+    lo2 = bf2_min(lo2, raw[i]);
+    hi2 = bf2_max(hi2, raw[i]);
+    ab2 = bf2_min_abs(ab2, raw[i]);
   }
 #pragma unroll
   for (int o = 1; o < 32 / NV; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+    lo2 = bf2_min(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+    hi2 = bf2_max(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+    ab2 = bf2_min_abs(ab2, __shfl_xor_sync(0xffffffffu, ab2, o));
   }
-  if (mag > 0x7E800000u) {              // above 2^126, infinite or NaN
+  const float lo = bf16lo_to_f32(bf2_min(lo2, swap_halves(lo2))) + 0.0f;   // -0 -> +0
+  const float hi = bf16lo_to_f32(bf2_max(hi2, swap_halves(hi2)));
+  const float mag = fmaxf(fabsf(lo), fabsf(hi));
+  const float small = fabsf(bf16lo_to_f32(bf2_min_abs(ab2, swap_halves(ab2))));
+  if (!(fabsf(lo) <= 0x1p126f && fabsf(hi) <= 0x1p126f)) {   // larger, infinite or NaN
     sz = kQ4NaN2;
     return 0u;
   }
-  lo += 0.0f;                           // -0 -> +0
   const uint32_t sb = q4_scale_bits(hi, lo);
   sz = sb | (__float_as_uint(lo) & 0xFFFF0000u);
   if (sb == 0u) return 0u;
   const float s = __uint_as_float(sb << 16);
-  const float inv = __fdividef(1.0f, s), half_s = 0.5f * s;
-  // four codes at a time as one integer below 2^16 in a float's mantissa
+  const float inv = __fdividef(1.0f, s);
+  constexpr float kMagic = 12582912.f;
+  float v[NV / 4];   // four codes as one integer below 2^16 in the mantissa of 2^23 + it
+#pragma unroll
+  for (int q = 0; q < NV / 4; ++q) v[q] = 8388608.f;
+  if (small * 32768.f >= mag) {
+    const float inv_up = inv * (1.0f + 0x1p-20f);
+    const uint32_t thr = __float_as_uint(-0.5f * s);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float x = i & 1 ? bf16hi_to_f32(raw[i / 2]) : bf16lo_to_f32(raw[i / 2]);
+      const float r = __fsub_rn(x, lo);
+      const float y = __fmaf_rn(r, inv_up, kMagic);
+      float n = __fsub_rn(y, kMagic);
+      const float d = __fmaf_rn(-n, s, r);
+      if (d <= __uint_as_float(thr | (~__float_as_uint(y) & 1u))) n = __fsub_rn(n, 1.0f);
+      v[i / 4] = __fmaf_rn(n, float(1 << (4 * (i & 3))), v[i / 4]);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i) {
+      uint32_t w = raw[0];
+#pragma unroll
+      for (int k = 1; k < NV / 2; ++k) w = i / 2 == k ? raw[k] : w;
+      const float n = q4_code_any(i & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w), lo, s, inv);
+      const float add = n * float(1 << (4 * (i & 3)));
+#pragma unroll
+      for (int q = 0; q < NV / 4; ++q) v[q] += i / 4 == q ? add : 0.f;
+    }
+  }
   uint32_t codes = 0;
 #pragma unroll
-  for (int q = 0; q < NV / 4; ++q) {
-    float v = 8388608.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v = __fmaf_rn(q4_code(x[4 * q + i], lo, s, half_s, inv), float(1 << (4 * i)), v);
-    codes |= (__float_as_uint(v) & 0xFFFFu) << (16 * q);
-  }
+  for (int q = 0; q < NV / 4; ++q) codes |= (__float_as_uint(v[q]) & 0xFFFFu) << (16 * q);
   return codes;
 }
 

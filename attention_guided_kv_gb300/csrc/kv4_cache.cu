@@ -5,8 +5,8 @@
 //   values of K and eight of V each: one 16-byte load a side, the group's
 //   minimum and maximum over four lanes by shuffles, one 4-byte store of codes
 //   a side and, from one lane in four, one of {scale, minimum}.  Nothing is
-//   read twice and every store is part of a full 64-byte row.  Bound by HBM:
-//   512 bytes read and 160 written a row.
+//   read twice and every store is part of a full 64-byte row: 512 bytes read
+//   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
 // evict: the select of h2o_evict.cu, then one cluster of 8 CTAs per
 //   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 448
@@ -23,7 +23,8 @@ namespace kvsel {
 
 constexpr int kQaThreads = 256;
 constexpr int kQaUnroll = 2;                          // rows a thread has in flight
-constexpr int kQaRows = kQaThreads / 16 * kQaUnroll;  // (token, kv head) rows a CTA takes at a time
+constexpr int kQaStep = kQaThreads / 16 * kQaUnroll;  // rows a CTA has in flight
+constexpr int kQaChunk = 256;                         // most rows a CTA looks up at once, one a thread
 
 struct Kv4Params {
   uint8_t* codes[2];   // K, V
@@ -35,6 +36,7 @@ struct Kv4Params {
   uint32_t* ticket;    // workspace: CTAs that are done with seq_lens
   int Hkv, max_pages, num_pages, page_lg, batch;
   int total;           // packed tokens
+  int chunk;           // (token, kv head) rows a CTA takes at a time: a multiple of kQaStep, at most kQaChunk
 };
 
 struct AppendParams : Kv4Params {
@@ -69,54 +71,76 @@ __device__ __forceinline__ int run_of(const Kv4Params& P, int b) {
   return a >= 0 && e >= a && e <= P.total ? e - a : -1;
 }
 
+// Pool row of packed (token, kv head) row r's slot, or -1: a row of no sequence
+// (nothing is reported) or one that does not fit.  `first`: the slot of a run's
+// first token; `limit`: the slots that it may take.
+template <class Place>
+__device__ __forceinline__ long long pool_row_of(const Kv4Params& P, uint32_t r, int end, Place place) {
+  const int t = int(r / uint32_t(P.Hkv)), g = int(r - uint32_t(t) * P.Hkv);
+  if (t >= end) return -1;
+  const int b = owner_of(P.tok_off, P.batch, t);
+  const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
+  long long slot = -1;
+  if (n >= 0 && at >= 0 && at < n) slot = place(b, g, n, at);
+  int phys = -1;
+  if (slot >= 0) phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
+  if (unsigned(phys) >= unsigned(P.num_pages)) {
+    report(P.status, KVSEL_ERR_BAD_INDEX);
+    return -1;
+  }
+  return (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & ((1 << P.page_lg) - 1));
+}
+
 __global__ void __launch_bounds__(kQaThreads) kv4_append_kernel(const AppendParams P) {
+  __shared__ long long s_row[2][kQaChunk];
   const int tid = threadIdx.x, l16 = tid & 15;
-  const uint32_t rows = uint32_t(P.total) * uint32_t(P.Hkv);   // < 2^31: checked on the host
-  const int page_mask = (1 << P.page_lg) - 1;
+  const uint32_t rows = uint32_t(P.total) * uint32_t(P.Hkv);   // < 2^31 - 2^20: checked on the host
   const long long capacity = (long long)P.max_pages << P.page_lg;
   const int end = __ldg(P.tok_off + P.batch);
+  int turn = 0;
 #pragma unroll 1
-  for (uint32_t r0 = blockIdx.x * kQaRows; r0 < rows; r0 += gridDim.x * kQaRows) {
+  for (uint32_t c0 = blockIdx.x * P.chunk; c0 < rows; c0 += gridDim.x * P.chunk, turn ^= 1) {
     uint4 kx[kQaUnroll], vx[kQaUnroll];
-    uint32_t rc[kQaUnroll];
+    auto load = [&](int step) {
 #pragma unroll
-    for (int u = 0; u < kQaUnroll; ++u) {
-      rc[u] = min(r0 + u * (kQaThreads / 16) + (tid >> 4), rows - 1);   // every lane takes part in the shuffles
-      kx[u] = __ldcs(P.k + size_t(rc[u]) * 16 + l16);
-      vx[u] = __ldcs(P.v + size_t(rc[u]) * 16 + l16);
-    }
-#pragma unroll
-    for (int u = 0; u < kQaUnroll; ++u) {
-      const bool in = r0 + u * (kQaThreads / 16) + (tid >> 4) < rows;
-      const int t = int(rc[u] / uint32_t(P.Hkv)), g = int(rc[u] - uint32_t(t) * P.Hkv);
-      const int b = owner_of(P.tok_off, P.batch, t);
-      const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
-      const int S = __ldcg(P.seq_lens + b);
-      bool ok = n >= 0 && at >= 0 && at < n && S >= 0 && (long long)S + n <= capacity &&
-                (P.max_len == 0 || (long long)S + n <= P.max_len);
-      long long row = 0;
-      const int slot = S + at;
-      if (ok) {
-        const int phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
-        ok = unsigned(phys) < unsigned(P.num_pages);
-        row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+      for (int u = 0; u < kQaUnroll; ++u) {
+        const uint32_t rc = min(c0 + step + u * (kQaThreads / 16) + (tid >> 4), rows - 1);   // every lane takes part in the shuffles
+        kx[u] = __ldcs(P.k + size_t(rc) * 16 + l16);
+        vx[u] = __ldcs(P.v + size_t(rc) * 16 + l16);
       }
-      // rows behind the last sequence are nobody's
-      if (in && !ok && t < end && l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
-      uint32_t sz[2], codes[2];
-      const uint32_t kr[4] = {kx[u].x, kx[u].y, kx[u].z, kx[u].w}, vr[4] = {vx[u].x, vx[u].y, vx[u].z, vx[u].w};
-      codes[0] = q4_group<8>(kr, sz[0]);
-      codes[1] = q4_group<8>(vr, sz[1]);
-      if (!in || !ok) continue;
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        reinterpret_cast<uint32_t*>(P.codes[side] + row * kQ4CodeBytes)[l16] = codes[side];
-        if ((l16 & 3) == 0) reinterpret_cast<uint32_t*>(P.scales[side] + row * kQ4ScaleBytes)[l16 >> 2] = sz[side];
-      }
-      if (l16 == 0) {
-        const size_t at_row = ((size_t)b * P.Hkv + g) * P.max_len + slot;
+    };
+    load(0);
+    if (tid < P.chunk && c0 + tid < rows)
+      s_row[turn][tid] = pool_row_of(P, c0 + tid, end, [&](int b, int g, int n, int at) -> long long {
+        const int S = __ldcg(P.seq_lens + b);
+        if (S < 0 || (long long)S + n > capacity || (P.max_len != 0 && (long long)S + n > P.max_len)) return -1;
+        const size_t at_row = ((size_t)b * P.Hkv + g) * P.max_len + S + at;
         if (P.pos_map) P.pos_map[at_row] = __ldcg(P.next_pos + b) + at;
         if (P.cum) P.cum[at_row] = 0.0f;
+        return (long long)S + at;
+      });
+    __syncthreads();   // the other buffer is read by the turn before
+#pragma unroll 1
+    for (int step = 0; step < P.chunk; step += kQaStep) {
+      uint32_t sz[kQaUnroll][2], codes[kQaUnroll][2];
+#pragma unroll
+      for (int u = 0; u < kQaUnroll; ++u) {
+        const uint32_t kr[4] = {kx[u].x, kx[u].y, kx[u].z, kx[u].w}, vr[4] = {vx[u].x, vx[u].y, vx[u].z, vx[u].w};
+        codes[u][0] = q4_group<8>(kr, sz[u][0]);
+        codes[u][1] = q4_group<8>(vr, sz[u][1]);
+      }
+      if (step + kQaStep < P.chunk) load(step + kQaStep);
+#pragma unroll
+      for (int u = 0; u < kQaUnroll; ++u) {
+        const int i = step + u * (kQaThreads / 16) + (tid >> 4);
+        if (c0 + i >= rows) continue;
+        const long long row = s_row[turn][i];
+        if (row < 0) continue;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          reinterpret_cast<uint32_t*>(P.codes[side] + row * kQ4CodeBytes)[l16] = codes[u][side];
+          if ((l16 & 3) == 0) reinterpret_cast<uint32_t*>(P.scales[side] + row * kQ4ScaleBytes)[l16 >> 2] = sz[u][side];
+        }
       }
     }
   }
@@ -143,59 +167,65 @@ __global__ void __launch_bounds__(kQaThreads) kv4_append_kernel(const AppendPara
 }
 
 __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P) {
+  __shared__ long long s_row[2][kQaChunk];
   const int tid = threadIdx.x, l16 = tid & 15;
   const uint32_t rows = uint32_t(P.total) * uint32_t(P.Hkv);
-  const int page_mask = (1 << P.page_lg) - 1;
   const long long capacity = (long long)P.max_pages << P.page_lg;
   const int end = __ldg(P.tok_off + P.batch);
+  int turn = 0;
 #pragma unroll 1
-  for (uint32_t r0 = blockIdx.x * kQaRows; r0 < rows; r0 += gridDim.x * kQaRows) {
-    uint32_t codes[kQaUnroll][2], sz[kQaUnroll][2], rr[kQaUnroll];
-    bool ok[kQaUnroll];
+  for (uint32_t c0 = blockIdx.x * P.chunk; c0 < rows; c0 += gridDim.x * P.chunk, turn ^= 1) {
+    if (tid < P.chunk && c0 + tid < rows)
+      s_row[turn][tid] = pool_row_of(P, c0 + tid, end, [&](int b, int, int, int at) -> long long {
+        const int S = __ldg(P.seq_lens + b), first = P.start ? __ldg(P.start + b) : 0;
+        const long long slot = (long long)first + at;
+        return first < 0 || slot >= S || slot >= capacity ? -1 : slot;
+      });
+    __syncthreads();   // the other buffer is read by the turn before
+    uint32_t codes[kQaUnroll][2], sz[kQaUnroll][2];
+    long long row[kQaUnroll];
+    auto load = [&](int step) {
 #pragma unroll
-    for (int u = 0; u < kQaUnroll; ++u) {
-      rr[u] = r0 + u * (kQaThreads / 16) + (tid >> 4);
-      const int t = int(rr[u] / uint32_t(P.Hkv)), g = int(rr[u] - uint32_t(t) * P.Hkv);
-      ok[u] = rr[u] < rows && t < end;    // rows behind the last sequence stay as they are
-      if (!ok[u]) continue;
-      const int b = owner_of(P.tok_off, P.batch, t);
-      const int n = run_of(P, b), at = t - __ldg(P.tok_off + b);
-      const int S = __ldg(P.seq_lens + b), first = P.start ? __ldg(P.start + b) : 0;
-      const long long slot = (long long)first + at;
-      bool good = n >= 0 && at >= 0 && at < n && first >= 0 && slot < S && slot < capacity;
-      int phys = -1;
-      if (good) {
-        phys = __ldg(P.block_table + (size_t)b * P.max_pages + (slot >> P.page_lg));
-        good = unsigned(phys) < unsigned(P.num_pages);
-      }
-      if (!good) {
-        if (l16 == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
-        ok[u] = false;
-        continue;
-      }
-      const long long row = (((long long)phys * P.Hkv + g) << P.page_lg) + (slot & page_mask);
+      for (int u = 0; u < kQaUnroll; ++u) {
+        const int i = step + u * (kQaThreads / 16) + (tid >> 4);
+        row[u] = c0 + i < rows ? s_row[turn][i] : -1;
+        if (row[u] < 0) continue;
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        codes[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.codes[side] + row * kQ4CodeBytes) + l16);
-        sz[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.scales[side] + row * kQ4ScaleBytes) + (l16 >> 2));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kQaUnroll; ++u) {
-      if (!ok[u]) continue;
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const float s = bf16lo_to_f32(sz[u][side]), z = bf16hi_to_f32(sz[u][side]);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          // the code in the mantissa of 2^23 + n, without a conversion
-          const float n = __uint_as_float(0x4B000000u | ((codes[u][side] >> (4 * i)) & 15u)) - 8388608.f;
-          x[i] = fmaf(n, s, z);
+        for (int side = 0; side < 2; ++side) {
+          codes[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.codes[side] + row[u] * kQ4CodeBytes) + l16);
+          sz[u][side] = __ldcs(reinterpret_cast<const uint32_t*>(P.scales[side] + row[u] * kQ4ScaleBytes) + (l16 >> 2));
         }
-        const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7]));
-        __stcs((side ? P.v : P.k) + size_t(rr[u]) * 16 + l16, o);
+      }
+    };
+    load(0);
+#pragma unroll 1
+    for (int step = 0; step < P.chunk; step += kQaStep) {
+      uint4 o[kQaUnroll][2];
+      bool have[kQaUnroll];
+#pragma unroll
+      for (int u = 0; u < kQaUnroll; ++u) {
+        have[u] = row[u] >= 0;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const float s = bf16lo_to_f32(sz[u][side]), z = bf16hi_to_f32(sz[u][side]);
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // the code in the mantissa of 2^23 + n, without a conversion
+            const float n = __uint_as_float(0x4B000000u | ((codes[u][side] >> (4 * i)) & 15u)) - 8388608.f;
+            x[i] = fmaf(n, s, z);
+          }
+          o[u][side] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                  pack_bf16x2(x[6], x[7]));
+        }
+      }
+      if (step + kQaStep < P.chunk) load(step + kQaStep);
+#pragma unroll
+      for (int u = 0; u < kQaUnroll; ++u) {
+        if (!have[u]) continue;
+        const size_t to = size_t(c0 + step + u * (kQaThreads / 16) + (tid >> 4)) * 16 + l16;
+        __stcs(P.k + to, o[u][0]);
+        __stcs(P.v + to, o[u][1]);
       }
     }
   }
@@ -313,6 +343,17 @@ kvsel_status check_kv4(const std::string& fn, const kvsel_paged_kv4* kv) {
   return KVSEL_OK;
 }
 
+// Rows a CTA takes at a time: few calls' rows are spread over the SMs, many
+// rows are looked up 256 at once.  Up to 8 CTAs an SM; more rows are strided over.
+int row_chunk(long long rows) {
+  const long long even = rows / ((long long)sm_count() * 4) / kQaStep * kQaStep;
+  return int(even < kQaStep ? kQaStep : even > kQaChunk ? kQaChunk : even);
+}
+int row_grid(long long rows, int chunk) {
+  const long long want = (rows + chunk - 1) / chunk, most = (long long)sm_count() * 8;
+  return int(want < most ? want : most);
+}
+
 void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages, int32_t* seq_lens, int batch,
           const int32_t* tok_off, int total, void* workspace) {
   P.codes[0] = static_cast<uint8_t*>(kv->k_codes);
@@ -330,12 +371,7 @@ void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, i
   P.page_lg = 4 + page_shift_of(kv->page_size);
   P.batch = batch;
   P.total = total;
-}
-
-// One CTA per kQaRows rows up to 8 CTAs an SM; more rows are strided over.
-int row_grid(long long rows) {
-  const long long want = (rows + kQaRows - 1) / kQaRows, most = (long long)sm_count() * 8;
-  return int(want < most ? want : most);
+  P.chunk = row_chunk((long long)total * kv->num_kv_heads);
 }
 
 struct Evict4Ws {
@@ -390,7 +426,7 @@ extern "C" kvsel_status kvsel_kv4_append(const kvsel_paged_kv4* kv, const int32_
   P.max_len = pos_map || h2o_cum ? max_len : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   trace_before("kv4_append", st);
-  kv4_append_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads), kQaThreads, 0, st>>>(P);
+  kv4_append_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads, P.chunk), kQaThreads, 0, st>>>(P);
   cudaError_t e = cudaGetLastError();
   trace_after(st);
   if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_append (launch)");
@@ -419,7 +455,7 @@ extern "C" kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t*
   P.v = static_cast<uint4*>(v_out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   trace_before("kv4_read", st);
-  kv4_read_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads), kQaThreads, 0, st>>>(P);
+  kv4_read_kernel<<<row_grid((long long)total_tokens * kv->num_kv_heads, P.chunk), kQaThreads, 0, st>>>(P);
   cudaError_t e = cudaGetLastError();
   trace_after(st);
   if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_read (launch)");
