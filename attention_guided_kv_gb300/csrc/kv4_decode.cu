@@ -17,9 +17,9 @@
 //   q is scaled per head by a power of two so that its largest magnitude is in
 // [2^14, 2^15): bf16 has 8 bits of mantissa, so fp16 then holds it exactly but
 // for values 2^-38 of the largest.  p s is scaled per group by a power of two
-// taken from the largest s seen so far (14 bits of headroom above fp16's
-// subnormals) and rounded to fp16: 2^-11 of its value at most, the step's only
-// rounding to 16 bits; the running maximum, the sums, the scores and the
+// taken from the largest s seen so far (p s < 2^14, with p up to 2^8) and
+// rounded to fp16: 2^-11 of its value at most, the step's only rounding to 16
+// bits; the running maximum, the sums, the scores and the
 // output accumulate in fp32.
 //
 // main kernel: one wave of warps; each takes an equal contiguous share of
@@ -48,8 +48,10 @@ namespace kvsel {
 
 constexpr int kQdWarps = 8;                 // warps of a CTA
 constexpr int kQdThreads = kQdWarps * 32;
+constexpr int kQdCtas = 2, kQdCtasWide = 1;  // CTAs an SM, up to 8 q heads a kv head and above
 constexpr int kQdTile = 32;                 // tokens of a tile
 constexpr int kQdMaxBatch = 1024;
+constexpr float kLag = 8.f;                 // see the running maximum
 constexpr int kQfSlots = 1024;              // finalize: slots per CTA
 constexpr int kQfThreads = 256;
 
@@ -112,6 +114,22 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16_16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D = A (16x8, row) * B (8x8, col), tf32 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_tf32_1688_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -147,7 +165,7 @@ __device__ __forceinline__ int checked_len(const Decode4Params& P, int b) {
 // kWide: more than 8 q heads a kv head (two blocks of 8 rows).  kMod: scores
 // are capped, biased or windowed, or positions come from a map.
 template <bool kWide, bool kMod, int kStages>
-__global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(const Decode4Params P) {
+__global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4_decode_kernel(const Decode4Params P) {
   constexpr int kH = kWide ? 2 : 1;
   extern __shared__ __align__(16) uint8_t qd_smem[];
   __shared__ int s_tiles[kQdMaxBatch + 1];   // exclusive prefix of the sequences' tile counts
@@ -205,6 +223,9 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
 
   QdStage* ring = reinterpret_cast<QdStage*>(qd_smem) + warp * kStages;
   const int page_mask = (1 << P.page_lg) - 1;
+  const uint8_t* codes_k = P.codes[0] + lane * 16;
+  const uint8_t* codes_v = P.codes[1] + lane * 16;
+  const uint8_t* scales_l = P.scales[lane >> 4] + (lane & 15) * kQ4ScaleBytes;
 
   // ---- one (sequence, kv head) pair after the other
 #pragma unroll 1
@@ -230,12 +251,14 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
     int32_t* prow = mapped ? P.pos_map + rowi * P.max_len : nullptr;
     const bool append = P.new_kv[0] != nullptr;
     int pos_q = S - 1;
+    float* lg = P.logits ? P.logits + ((size_t)b * P.Hq + kvh * P.G + 2 * t4) * P.max_len + g8 : nullptr;
     if (kMod && mapped) pos_q = append ? __ldcg(P.next_pos + b) : __ldcg(prow + S - 1);
 
     // q: fragments of head g8 (+ 8), scaled by a power of two; group sums and factors of the heads
     // 2 t4, 2 t4 + 1 (+ 8) whose scores this thread holds
     uint32_t qa[kH][4][4];   // per group: {dims 0,4}, {1,5}/16, {2,6}, {3,7}/16 of the thread's word
-    float qs[kH][4][2], mult[kH][2], slope[kH][2];
+    uint32_t qz[kH][2];      // sum of q over group t4 of head g8 (+ 8), as two tf32 numbers (22 bits)
+    float mult[kH][2], slope[kH][2];
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       const int head = g8 + 8 * h;
@@ -255,7 +278,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       // largest magnitude in [2^(e-127), 2^(e-126)), e = top >> 23; q' = q 2^(14-(e-127))
       const int e = max(int(top >> 23), 15);
       const float up = __uint_as_float(uint32_t(268 - e) << 23);   // 13 <= 268 - e <= 253
-      float sums[4];
+      float own_sum = 0.f;
 #pragma unroll
       for (int gq = 0; gq < 4; ++gq) {
         const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
@@ -272,8 +295,10 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
         qa[h][gq][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        sums[gq] = sum * 0x1p-24f;   // as if it had come out of the product with the codes
+        if (gq == t4) own_sum = sum * 0x1p-24f;   // as if it had come out of the product with the codes
       }
+      qz[h][0] = __float_as_uint(own_sum) & 0xFFFFE000u;
+      qz[h][1] = __float_as_uint(own_sum - __uint_as_float(qz[h][0])) & 0xFFFFE000u;
       // a product with the codes is 2^(141-e-24) times the true one
       float f = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
       const float sl = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
@@ -281,8 +306,6 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int from = 8 * t4 + 4 * k;   // a lane of head 2 t4 + k
-#pragma unroll
-        for (int gq = 0; gq < 4; ++gq) qs[h][gq][k] = __shfl_sync(0xffffffffu, sums[gq], from);
         mult[h][k] = __shfl_sync(0xffffffffu, f, from);
         slope[h][k] = kMod ? __shfl_sync(0xffffffffu, sl, from) : 0.f;
       }
@@ -324,17 +347,17 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const bool ok = unsigned(ph[half]) < unsigned(P.num_pages);
-        const size_t base = ((((size_t)(ok ? ph[half] : 0) * P.Hkv + kvh)) << P.page_lg) + ((s0 + 16 * half) & page_mask);
+        const uint32_t base = ((uint32_t(ok ? ph[half] : 0) * P.Hkv + kvh) << P.page_lg) + ((s0 + 16 * half) & page_mask);
         const int bytes = ok ? 16 : 0;
-        const uint8_t* ck = P.codes[0] + base * kQ4CodeBytes + lane * 16;
-        const uint8_t* cv = P.codes[1] + base * kQ4CodeBytes + lane * 16;
+        const uint8_t* ck = codes_k + (size_t)base * kQ4CodeBytes;
+        const uint8_t* cv = codes_v + (size_t)base * kQ4CodeBytes;
         const uint32_t dk = smem_u32(st.k) + half * 1024 + c_dst, dv = smem_u32(st.v) + half * 1024 + c_dst;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk + k * 512), "l"(ck + k * 512), "r"(bytes) : "memory");
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dv + k * 512), "l"(cv + k * 512), "r"(bytes) : "memory");
         }
-        const uint8_t* sc = P.scales[lane >> 4] + (base + (lane & 15)) * kQ4ScaleBytes;
+        const uint8_t* sc = scales_l + (size_t)base * kQ4ScaleBytes;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32((lane >> 4 ? st.vs : st.ks) + 16 * half + (lane & 15))), "l"(sc), "r"(bytes) : "memory");
       }
       if (kMod && mapped) {
@@ -450,36 +473,47 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
 
       // ---- scores: tokens 8 r + g8 x heads 2 t4, 2 t4 + 1 (+ 8)
       float x[kH][4][2];
+      // this lane's row of an 8-row ldmatrix, chunk lane >> 3: rows 8 on have the same swizzle
+      const uint32_t ld_off = (lane & 7) * kQ4CodeBytes + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+      const uint32_t k_base = smem_u32(st.k) + ld_off, v_base = smem_u32(st.v) + ld_off;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         // words t4 of groups 0..3 of tokens 16 mt + g8 and + 8
         uint32_t w[2][4];
         uint4 sz[2];
+        uint32_t zt[2];   // minimum of group t4 of the two tokens
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = 16 * mt + 8 * r + (lane & 7), c = lane >> 3;
-          ldsm_x4(smem_u32(st.k + row * kQ4CodeBytes + ((c ^ ((row >> 1) & 3)) << 4)), w[r][0], w[r][1], w[r][2], w[r][3]);
+          ldsm_x4(k_base + (16 * mt + 8 * r) * kQ4CodeBytes, w[r][0], w[r][1], w[r][2], w[r][3]);
           sz[r] = st.ks[16 * mt + 8 * r + g8];
+          zt[r] = reinterpret_cast<const uint32_t*>(st.ks)[(16 * mt + 8 * r) * 4 + lane] & 0xFFFF0000u;
         }
         const uint32_t s0w[4] = {sz[0].x, sz[0].y, sz[0].z, sz[0].w}, s1w[4] = {sz[1].x, sz[1].y, sz[1].z, sz[1].w};
+        // the minima's part, z (sum of q): a product over the groups
 #pragma unroll
-        for (int h = 0; h < kH; ++h) x[h][2 * mt][0] = x[h][2 * mt][1] = x[h][2 * mt + 1][0] = x[h][2 * mt + 1][1] = 0.f;
+        for (int h = 0; h < kH; ++h) {
+          float c[4];
+          mma_tf32_1688_zero(c, zt[0], zt[1], zt[0], zt[1], qz[h][0], qz[h][1]);
+          x[h][2 * mt][0] = c[0];
+          x[h][2 * mt][1] = c[1];
+          x[h][2 * mt + 1][0] = c[2];
+          x[h][2 * mt + 1][1] = c[3];
+        }
 #pragma unroll
         for (int gq = 0; gq < 4; ++gq) {
           const uint32_t u0 = w[0][gq] >> 8, u1 = w[1][gq] >> 8;
           const uint32_t a[8] = {w[0][gq] & 0x000F000Fu, w[1][gq] & 0x000F000Fu, w[0][gq] & 0x00F000F0u, w[1][gq] & 0x00F000F0u,
                                  u0 & 0x000F000Fu,       u1 & 0x000F000Fu,       u0 & 0x00F000F0u,       u1 & 0x00F000F0u};
-          const float sa = bf16lo_to_f32(s0w[gq]), za = bf16hi_to_f32(s0w[gq]);
-          const float sb = bf16lo_to_f32(s1w[gq]), zb = bf16hi_to_f32(s1w[gq]);
+          const float sa = bf16lo_to_f32(s0w[gq]), sb = bf16lo_to_f32(s1w[gq]);
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(c, a[0], a[1], a[2], a[3], qa[h][gq][0], qa[h][gq][1]);
+            float c[4];
+            mma_f16_16816_zero(c, a[0], a[1], a[2], a[3], qa[h][gq][0], qa[h][gq][1]);
             mma_f16_16816(c, a[4], a[5], a[6], a[7], qa[h][gq][2], qa[h][gq][3]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              x[h][2 * mt][k] = fmaf(sa, c[k], fmaf(za, qs[h][gq][k], x[h][2 * mt][k]));
-              x[h][2 * mt + 1][k] = fmaf(sb, c[2 + k], fmaf(zb, qs[h][gq][k], x[h][2 * mt + 1][k]));
+              x[h][2 * mt][k] = fmaf(sa, c[k], x[h][2 * mt][k]);
+              x[h][2 * mt + 1][k] = fmaf(sb, c[2 + k], x[h][2 * mt + 1][k]);
             }
           }
         }
@@ -500,14 +534,19 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
                 y = fmaf(-slope[h][k], fabsf(float(pos_q - p)), y);
               }
             }
-            x[h][r][k] = (vis_own >> (8 * r)) & 1u ? y : -INFINITY;
+            x[h][r][k] = y;
           }
+        if (vis != 0xffffffffu) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) x[h][r][k] = (vis_own >> (8 * r)) & 1u ? x[h][r][k] : -INFINITY;
+        }
         if (P.logits) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int head = 8 * h + 2 * t4 + k;
-            if (head < P.G) {
-              float* lrow = P.logits + ((size_t)b * P.Hq + kvh * P.G + head) * P.max_len + s0 + g8;
+          for (int k = 0; k < 2; ++k)
+            if (8 * h + 2 * t4 + k < P.G) {
+              float* lrow = lg + (size_t)(8 * h + k) * P.max_len + s0;
               if (s0 + kQdTile <= S) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) lrow[8 * r] = x[h][r][k];
@@ -517,19 +556,18 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
                   if (s0 + 8 * r + g8 < S) lrow[8 * r] = x[h][r][k];
               }
             }
-          }
         }
-        // running maximum and sum
+        // m follows the maximum once it lags by more than kLag powers of two: p = 2^(x - m) up to 2^kLag is as
+        // good as p up to 1, and most tiles need no reduction over the tokens
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float mx = fmaxf(fmaxf(x[h][0][k], x[h][1][k]), fmaxf(x[h][2][k], x[h][3][k]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx, m[h][k]);
-          const float use = mx == -INFINITY ? 0.f : mx;
-          if (__any_sync(0xffffffffu, mx > m[h][k])) {
-            const float corr = ex2(m[h][k] - use);
+          if (__any_sync(0xffffffffu, mx > m[h][k] + kLag || (m[h][k] == -INFINITY && mx > m[h][k]))) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx, m[h][k]);
+            const float corr = mx == -INFINITY ? 1.f : ex2(m[h][k] - mx);
             m[h][k] = mx;
             l[h][k] *= corr;
 #pragma unroll
@@ -539,6 +577,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
               for (int q = 0; q < 4; ++q) o[h][gq][2 * q + k] *= corr;   // columns are heads too
             }
           }
+          const float use = m[h][k] == -INFINITY ? 0.f : m[h][k];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             x[h][r][k] = ex2(x[h][r][k] - use);
@@ -550,7 +589,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
       // ---- output: (dims x tokens) codes times (tokens x heads) p s, per group
       float inv_e[4];
 #pragma unroll
-      for (int gq = 0; gq < 4; ++gq) inv_e[gq] = __uint_as_float(uint32_t(268 - e_v[gq]) << 23);
+      for (int gq = 0; gq < 4; ++gq) inv_e[gq] = __uint_as_float(uint32_t(260 - e_v[gq]) << 23);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t pb[kH][4][2];
@@ -574,10 +613,8 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
         // halves g8 of groups 0..3, tokens 2 t4 and 2 t4 + 1 of the 8 (lo) and the next 8 (hi)
         uint32_t lo[4], hi[4];
         {
-          const int row = 16 * mt + (lane & 7), c = lane >> 3;
-          const int off = ((c ^ ((row >> 1) & 3)) << 4);
-          ldsm_x4_t(smem_u32(st.v + row * kQ4CodeBytes + off), lo[0], lo[1], lo[2], lo[3]);
-          ldsm_x4_t(smem_u32(st.v + (row + 8) * kQ4CodeBytes + off), hi[0], hi[1], hi[2], hi[3]);
+          ldsm_x4_t(v_base + 16 * mt * kQ4CodeBytes, lo[0], lo[1], lo[2], lo[3]);
+          ldsm_x4_t(v_base + (16 * mt + 8) * kQ4CodeBytes, hi[0], hi[1], hi[2], hi[3]);
         }
 #pragma unroll
         for (int gq = 0; gq < 4; ++gq) {
@@ -621,9 +658,9 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? 1 : 2) kv4_decode_kernel(c
           z[k] += __shfl_xor_sync(0xffffffffu, z[k], 8);
           z[k] += __shfl_xor_sync(0xffffffffu, z[k], 16);
         }
-        // codes were n 2^-24 (dims 0, 2) and n 2^-20 (dims 1, 3), p s was p s 2^(141 - e): undone in
+        // codes were n 2^-24 (dims 0, 2) and n 2^-20 (dims 1, 3), p s was p s 2^(133 - e): undone in
         // two factors so that neither overflows
-        const float back = __uint_as_float(uint32_t(e_v[gq] - 14) << 23);
+        const float back = __uint_as_float(uint32_t(e_v[gq] - 6) << 23);
         const float* a = o[h][gq];
         const float c24 = 0x1p24f, c20 = 0x1p20f;
         float* po = P.part_o + (slot * P.G + head) * kQ4D + 32 * gq + 4 * g8;
@@ -796,9 +833,8 @@ struct Decode4Ws {
   size_t eff_off, pre_off, ml_off, o_off, logits_off, total;
 };
 
-// CTAs of the main kernel: every co-resident slot (8 warps each; two CTAs an
-// SM up to 8 q heads a kv head, one above).
-int decode4_ctas(int G) { return sm_count() * (G > 8 ? 1 : 2); }
+// CTAs of the main kernel: every co-resident slot.
+int decode4_ctas(int G) { return sm_count() * (G > 8 ? kQdCtasWide : kQdCtas); }
 
 // The workspace is sized for the largest grid the device could take; the
 // number of SMs is that of the current device.
@@ -823,6 +859,8 @@ kvsel_status check_shape(const std::string& fn, const kvsel_paged_kv4* kv) {
     return fail(KVSEL_ERR_UNSUPPORTED, fn + "only head_dim 128 and page_size 16, 32, 64, 128 or 256 are implemented");
   if (kv->num_q_heads / kv->num_kv_heads > 16)
     return fail(KVSEL_ERR_UNSUPPORTED, fn + "at most 16 q heads per kv head are implemented");
+  if ((long long)kv->num_pages * kv->num_kv_heads * kv->page_size >= (1ll << 31))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "num_pages * num_kv_heads * page_size must be below 2^31");
   return KVSEL_OK;
 }
 

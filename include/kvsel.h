@@ -749,7 +749,8 @@ KVSEL_API kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t* 
  *   probs        entries j >= S_b are not written; keys that are not seen get 0.
  *   workspace    >= kvsel_kv4_decode_attn_workspace(...) bytes, zeroed before
  *                first use; calls that may overlap need workspaces of their own.
- * num_q_heads / num_kv_heads <= 16, batch <= 1024 (else UNSUPPORTED / INVALID).
+ * num_q_heads / num_kv_heads <= 16 and num_pages * num_kv_heads * page_size <
+ * 2^31 (else UNSUPPORTED), batch <= 1024 (else INVALID_ARG).
  * A length that is negative or does not fit the table or max_len records
  * KVSEL_ERR_BAD_INDEX and nothing is computed for that sequence; keys on a page
  * outside the pool record it too and are not seen.  Two launches. */
