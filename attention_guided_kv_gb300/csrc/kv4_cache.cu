@@ -9,12 +9,13 @@
 //   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
 // evict: the select of h2o_evict.cu, then one cluster of 8 CTAs per
-//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 448
-//   kept rows in the cluster's shared memory, waits for the whole cluster and
+//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 128 kept
+//   rows in the cluster's shared memory, waits for the whole cluster and
 //   writes them to their new slots; kept lists are ascending, so keep[i] >= i
-//   and a round never writes a slot that a later round still reads.  One
-//   barrier per round is the only ordering; a CTA per row, as the bf16
-//   cache's compaction has it, leaves most SMs idle at 64 rows.
+//   and a round never writes a slot that a later round still reads, which lets
+//   the next round's rows load meanwhile.  One cluster barrier a round is the
+//   only ordering; one CTA per (sequence, kv head), as the bf16 cache's
+//   compaction has it, leaves most SMs idle at 64 of them.
 #include "common.cuh"
 #include "h2o_select.cuh"
 #include "kv4.cuh"
@@ -235,8 +236,8 @@ __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P
 // compaction
 // ---------------------------------------------------------------------------
 constexpr int kQcCluster = 8;
-constexpr int kQcRows = 448;     // kept rows a CTA stages per round
-constexpr int kQcThreads = 512;
+constexpr int kQcRows = 128;     // kept rows a CTA stages per round
+constexpr int kQcThreads = 256;
 constexpr int kQcUnits = 10;     // 16-byte units of a row: K codes 4, V codes 4, K and V scales
 
 struct Compact4Params {
@@ -252,7 +253,7 @@ struct Compact4Params {
   int Hkv, max_len, max_pages, num_pages, budget, page_lg;
 };
 
-struct Compact4Smem {
+struct Compact4Stage {
   uint4 unit[kQcRows][kQcUnits];
   long long src[kQcRows], dst[kQcRows];  // pool rows, -1: a bad table entry
   float cum[kQcRows];
@@ -261,7 +262,7 @@ struct Compact4Smem {
 
 __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4Params P) {
   extern __shared__ __align__(16) uint8_t qc_smem[];
-  Compact4Smem& sm = *reinterpret_cast<Compact4Smem*>(qc_smem);
+  Compact4Stage* const stages = reinterpret_cast<Compact4Stage*>(qc_smem);   // two
   const int rank = blockIdx.x % kQcCluster, kvh = blockIdx.x / kQcCluster, b = blockIdx.y, tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept lists come from the select
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
@@ -285,12 +286,16 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
     }
     return (((long long)phys * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);
   };
-#pragma unroll 1
-  for (int c0 = P.first_move[rowi]; c0 < P.budget; c0 += kQcCluster * kQcRows) {
-    // an even share of the round's rows for every CTA of the cluster
+  // This CTA's rows of the round that starts at c0: an even share for every CTA of the cluster.
+  auto share_of = [&](int c0, int& i0) {
     const int left = min(kQcCluster * kQcRows, P.budget - c0);
     const int share = (left + kQcCluster - 1) / kQcCluster;
-    const int i0 = c0 + rank * share, cnt = max(0, min(share, left - rank * share));
+    i0 = c0 + rank * share;
+    return max(0, min(share, left - rank * share));
+  };
+  auto start = [&](int c0, Compact4Stage& sm) {   // its rows come into shared memory
+    int i0;
+    const int cnt = share_of(c0, i0);
     for (int i = tid; i < cnt; i += kQcThreads) {
       const int src = keep[i0 + i];
       sm.src[i] = pool_row(src);
@@ -306,9 +311,26 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
       const uint8_t* from = w < 8 ? P.codes[w >> 2] + row * kQ4CodeBytes + (w & 3) * 16 : P.scales[w - 8] + row * kQ4ScaleBytes;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[i][w])), "l"(from) : "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  constexpr int kRound = kQcCluster * kQcRows;
+  int c0 = P.first_move[rowi], turn = 0;
+  if (c0 < P.budget) start(c0, stages[0]);
+#pragma unroll 1
+  for (; c0 < P.budget; c0 += kRound, turn ^= 1) {
+    // the next round's rows are on their way while this one's are written: they lie behind every slot
+    // that this round writes
+    if (c0 + kRound < P.budget) {
+      start(c0 + kRound, stages[turn ^ 1]);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
     // all of the round's sources are in shared memory before any of its slots is written
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    Compact4Stage& sm = stages[turn];
+    int i0;
+    const int cnt = share_of(c0, i0);
     for (int u = tid; u < cnt * kQcUnits; u += kQcThreads) {
       const int i = u / kQcUnits, w = u - i * kQcUnits;
       const long long row = sm.dst[i];
@@ -320,7 +342,7 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
       crow[i0 + i] = sm.cum[i];
       if (prow) prow[i0 + i] = sm.pos[i];
     }
-    __syncthreads();
+    __syncthreads();   // the stage is free for the round after the next
   }
 }
 
@@ -523,14 +545,14 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   C.num_pages = kv->num_pages;
   C.budget = budget;
   C.page_lg = 4 + page_shift_of(kv->page_size);
-  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(sizeof(Compact4Smem)));
+  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(2 * sizeof(Compact4Stage)));
       e != cudaSuccess)
     return cuda_fail(e, "kvsel_kv4_evict (attribute)");
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(kv->num_kv_heads) * kQcCluster, batch);
   cfg.blockDim = dim3(kQcThreads);
-  cfg.dynamicSmemBytes = sizeof(Compact4Smem);
+  cfg.dynamicSmemBytes = 2 * sizeof(Compact4Stage);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

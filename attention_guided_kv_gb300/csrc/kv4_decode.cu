@@ -46,9 +46,10 @@
 
 namespace kvsel {
 
-constexpr int kQdWarps = 8;                 // warps of a CTA
-constexpr int kQdThreads = kQdWarps * 32;
-constexpr int kQdCtas = 2, kQdCtasWide = 1;  // CTAs an SM, up to 8 q heads a kv head and above
+// Warps of a CTA, one CTA an SM, up to 8 q heads a kv head and above.  Fewer warps with more registers
+// (168) beat more of them: at 8 x 32K, 64/8 heads, 12 warps take 73 us, 16 (128 registers, some spilled) 89,
+// 20 (96) 134, and 8 with four stages 79.
+constexpr int kQdWarps = 12, kQdWarpsWide = 8;
 constexpr int kQdTile = 32;                 // tokens of a tile
 constexpr int kQdMaxBatch = 1024;
 constexpr float kLag = 8.f;                 // see the running maximum
@@ -135,6 +136,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 16 bytes into shared memory, zeros if bytes is 0; the cache is read once, so its lines leave L2 first
+// (the scores, which the second kernel reads back, stay).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(pol)
+               : "memory");
+}
+
 // Tiles of a sequence that hold a key its query may see, in order: the sink
 // tiles, then those of the window (all of them without a window, or where
 // positions come from a map).
@@ -165,11 +173,12 @@ __device__ __forceinline__ int checked_len(const Decode4Params& P, int b) {
 // kWide: more than 8 q heads a kv head (two blocks of 8 rows).  kMod: scores
 // are capped, biased or windowed, or positions come from a map.
 template <bool kWide, bool kMod, int kStages>
-__global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4_decode_kernel(const Decode4Params P) {
-  constexpr int kH = kWide ? 2 : 1;
+__global__ void __launch_bounds__((kWide ? kQdWarpsWide : kQdWarps) * 32, 1) kv4_decode_kernel(const Decode4Params P) {
+  constexpr int kH = kWide ? 2 : 1, kW = kWide ? kQdWarpsWide : kQdWarps, kThreads = kW * 32;
   extern __shared__ __align__(16) uint8_t qd_smem[];
   __shared__ int s_tiles[kQdMaxBatch + 1];   // exclusive prefix of the sequences' tile counts
-  __shared__ int s_scan[kQdWarps];
+  __shared__ int s_len[kQdMaxBatch];
+  __shared__ int s_scan[kW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
   const bool mapped = P.pos_map != nullptr;
@@ -177,16 +186,16 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
 
   // ---- the share of this warp
   int carry = 0;
-  for (int b0 = 0; b0 < P.B; b0 += kQdThreads) {
+  for (int b0 = 0; b0 < P.B; b0 += kThreads) {
     const int b = b0 + tid;
-    int n = 0;
+    int n = 0, S_b = 0;
     if (b < P.B) {
-      const int S = checked_len(P, b);
+      S_b = checked_len(P, b);
       if (blockIdx.x == 0) {
-        P.eff_len[b] = S;
-        if (S < 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+        P.eff_len[b] = S_b;
+        if (S_b < 0) report(P.status, KVSEL_ERR_BAD_INDEX);
       }
-      n = S > 0 ? tiles_of(S, P.window, P.n_sink, mapped).count : 0;
+      n = S_b > 0 ? tiles_of(S_b, P.window, P.n_sink, mapped).count : 0;
     }
     int x = n;
 #pragma unroll
@@ -198,12 +207,13 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
     __syncthreads();
     int base = carry, sum = carry;
 #pragma unroll
-    for (int w = 0; w < kQdWarps; ++w) {
+    for (int w = 0; w < kW; ++w) {
       if (w < warp) base += s_scan[w];
       sum += s_scan[w];
     }
     if (b < P.B) {
       s_tiles[b] = base + x - n;
+      s_len[b] = S_b;
       if (blockIdx.x == 0) P.tile_pre[b] = base + x - n;
     }
     carry = sum;
@@ -216,13 +226,14 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
   __syncthreads();
   const long long T = (long long)carry * P.Hkv;
   const long long N = min((long long)P.warps, T);
-  const long long wid = (long long)blockIdx.x * kQdWarps + warp;
+  const long long wid = (long long)blockIdx.x * kW + warp;
   if (wid >= N) return;
   long long tile = wid * T / N;
   const long long tile_end = (wid + 1) * T / N;
 
   QdStage* ring = reinterpret_cast<QdStage*>(qd_smem) + warp * kStages;
   const int page_mask = (1 << P.page_lg) - 1;
+  const uint64_t pol = l2_policy_evict_first();
   const uint8_t* codes_k = P.codes[0] + lane * 16;
   const uint8_t* codes_v = P.codes[1] + lane * 16;
   const uint8_t* scales_l = P.scales[lane >> 4] + (lane & 15) * kQ4ScaleBytes;
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
     const long long in_b = tile - (long long)s_tiles[b] * P.Hkv;
     const int kvh = int(in_b / nb), i0 = int(in_b - (long long)kvh * nb);
     const int i1 = int(min((long long)nb, i0 + (tile_end - tile)));
-    const int S = checked_len(P, b);
+    const int S = s_len[b];
     const TileSet ts = tiles_of(S, P.window, P.n_sink, mapped);
     const int32_t* bt = P.block_table + (size_t)b * P.max_pages;
     const size_t rowi = (size_t)b * P.Hkv + kvh;
@@ -254,63 +265,16 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
     float* lg = P.logits ? P.logits + ((size_t)b * P.Hq + kvh * P.G + 2 * t4) * P.max_len + g8 : nullptr;
     if (kMod && mapped) pos_q = append ? __ldcg(P.next_pos + b) : __ldcg(prow + S - 1);
 
-    // q: fragments of head g8 (+ 8), scaled by a power of two; group sums and factors of the heads
-    // 2 t4, 2 t4 + 1 (+ 8) whose scores this thread holds
-    uint32_t qa[kH][4][4];   // per group: {dims 0,4}, {1,5}/16, {2,6}, {3,7}/16 of the thread's word
-    uint32_t qz[kH][2];      // sum of q over group t4 of head g8 (+ 8), as two tf32 numbers (22 bits)
-    float mult[kH][2], slope[kH][2];
+    // q first, so that it is on its way while the copies are set up
+    uint4 raw_q[kH][4];
 #pragma unroll
-    for (int h = 0; h < kH; ++h) {
-      const int head = g8 + 8 * h;
-      uint4 raw[4];
-      uint32_t top = 0;
+    for (int h = 0; h < kH; ++h)
 #pragma unroll
       for (int gq = 0; gq < 4; ++gq) {
-        raw[gq] = make_uint4(0, 0, 0, 0);
-        if (head < P.G)
-          raw[gq] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)b * P.Hq + kvh * P.G + head) * kQ4D + 32 * gq + 8 * t4));
-        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max((r[i] << 16) & 0x7F800000u, r[i] & 0x7F800000u));
+        raw_q[h][gq] = make_uint4(0, 0, 0, 0);
+        if (g8 + 8 * h < P.G)
+          raw_q[h][gq] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)b * P.Hq + kvh * P.G + g8 + 8 * h) * kQ4D + 32 * gq + 8 * t4));
       }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // largest magnitude in [2^(e-127), 2^(e-126)), e = top >> 23; q' = q 2^(14-(e-127))
-      const int e = max(int(top >> 23), 15);
-      const float up = __uint_as_float(uint32_t(268 - e) << 23);   // 13 <= 268 - e <= 253
-      float own_sum = 0.f;
-#pragma unroll
-      for (int gq = 0; gq < 4; ++gq) {
-        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
-        float x[8], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = bf16lo_to_f32(r[i]) * up;
-          x[2 * i + 1] = bf16hi_to_f32(r[i]) * up;
-          sum += x[2 * i] + x[2 * i + 1];
-        }
-        qa[h][gq][0] = pack_f16x2(x[0], x[4]);
-        qa[h][gq][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
-        qa[h][gq][2] = pack_f16x2(x[2], x[6]);
-        qa[h][gq][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (gq == t4) own_sum = sum * 0x1p-24f;   // as if it had come out of the product with the codes
-      }
-      qz[h][0] = __float_as_uint(own_sum) & 0xFFFFE000u;
-      qz[h][1] = __float_as_uint(own_sum - __uint_as_float(qz[h][0])) & 0xFFFFE000u;
-      // a product with the codes is 2^(141-e-24) times the true one
-      float f = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
-      const float sl = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
-      if (!kMod) f *= kLog2e;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int from = 8 * t4 + 4 * k;   // a lane of head 2 t4 + k
-        mult[h][k] = __shfl_sync(0xffffffffu, f, from);
-        slope[h][k] = kMod ? __shfl_sync(0xffffffffu, sl, from) : 0.f;
-      }
-    }
-
     float m[kH][2], l[kH][2], zacc[kH][4][2], o[kH][4][8];
     int e_v[4];               // per group: 2^(e_v - 127) is above every value scale so far
 #pragma unroll
@@ -354,11 +318,11 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
         const uint32_t dk = smem_u32(st.k) + half * 1024 + c_dst, dv = smem_u32(st.v) + half * 1024 + c_dst;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dk + k * 512), "l"(ck + k * 512), "r"(bytes) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dv + k * 512), "l"(cv + k * 512), "r"(bytes) : "memory");
+          copy16(dk + k * 512, ck + k * 512, bytes, pol);
+          copy16(dv + k * 512, cv + k * 512, bytes, pol);
         }
         const uint8_t* sc = scales_l + (size_t)base * kQ4ScaleBytes;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32((lane >> 4 ? st.vs : st.ks) + 16 * half + (lane & 15))), "l"(sc), "r"(bytes) : "memory");
+        copy16(smem_u32((lane >> 4 ? st.vs : st.ks) + 16 * half + (lane & 15)), sc, bytes, pol);
       }
       if (kMod && mapped) {
         const int s = s0 + lane;
@@ -378,6 +342,60 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
     pages_of(i0 + kStages - 1, ph_next);
+
+    // q: fragments of head g8 (+ 8), scaled by a power of two; group sums and factors of the heads
+    // 2 t4, 2 t4 + 1 (+ 8) whose scores this thread holds
+    uint32_t qa[kH][4][4];   // per group: {dims 0,4}, {1,5}/16, {2,6}, {3,7}/16 of the thread's word
+    uint32_t qz[kH][2];      // sum of q over group t4 of head g8 (+ 8), as two tf32 numbers (22 bits)
+    float mult[kH][2], slope[kH][2];
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      const int head = g8 + 8 * h;
+      const uint4(&raw)[4] = raw_q[h];
+      uint32_t top = 0;
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max((r[i] << 16) & 0x7F800000u, r[i] & 0x7F800000u));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest magnitude in [2^(e-127), 2^(e-126)), e = top >> 23; q' = q 2^(14-(e-127))
+      const int e = max(int(top >> 23), 15);
+      const float up = __uint_as_float(uint32_t(268 - e) << 23);   // 13 <= 268 - e <= 253
+      float own_sum = 0.f;
+#pragma unroll
+      for (int gq = 0; gq < 4; ++gq) {
+        const uint32_t r[4] = {raw[gq].x, raw[gq].y, raw[gq].z, raw[gq].w};
+        float x[8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = bf16lo_to_f32(r[i]) * up;
+          x[2 * i + 1] = bf16hi_to_f32(r[i]) * up;
+          sum += x[2 * i] + x[2 * i + 1];
+        }
+        qa[h][gq][0] = pack_f16x2(x[0], x[4]);
+        qa[h][gq][1] = pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f);
+        qa[h][gq][2] = pack_f16x2(x[2], x[6]);
+        qa[h][gq][3] = pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (gq == t4) own_sum = sum * 0x1p-24f;   // as if it had come out of the product with the codes
+      }
+      qz[h][0] = __float_as_uint(own_sum) & 0xFFFFE000u;
+      qz[h][1] = __float_as_uint(own_sum - __uint_as_float(qz[h][0])) & 0xFFFFE000u;
+      // a product with the codes is 2^(141-e-24) times the true one
+      float f = P.scale * 0x1p24f * __uint_as_float(uint32_t(e - 14) << 23);
+      const float sl = kMod && P.slopes && head < P.G ? __ldg(P.slopes + kvh * P.G + head) * kLog2e : 0.f;
+      if (!kMod) f *= kLog2e;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int from = 8 * t4 + 4 * k;   // a lane of head 2 t4 + k
+        mult[h][k] = __shfl_sync(0xffffffffu, f, from);
+        slope[h][k] = kMod ? __shfl_sync(0xffffffffu, sl, from) : 0.f;
+      }
+    }
 
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
@@ -430,22 +448,25 @@ __global__ void __launch_bounds__(kQdThreads, kWide ? kQdCtasWide : kQdCtas) kv4
       }
 
       // ---- which of the 32 keys are seen (lane t: token t)
-      uint32_t vis;
+      uint32_t vis = 0xffffffffu;
       {
-        const int s = s0 + lane;
-        const bool live = s < S, paged = unsigned(lane < 16 ? ph0 : ph1) < unsigned(P.num_pages);
-        bool see = live && paged;
-        if (live && !paged) report(P.status, KVSEL_ERR_BAD_INDEX);
-        if (kMod && P.window > 0) {
-          const int p = mapped ? st.pos[lane] : s;
-          see = see && (pos_q - p < P.window || p < P.n_sink);
-        }
-        vis = __ballot_sync(0xffffffffu, see);
-        // what is not seen must not reach the product with p = 0 as NaN or infinity
         uint4 own = st.vs[lane];
-        if (!see) {
-          own = make_uint4(0, 0, 0, 0);
-          st.vs[lane] = own;
+        const bool inner = s0 + kQdTile <= S && unsigned(ph0) < unsigned(P.num_pages) && unsigned(ph1) < unsigned(P.num_pages);
+        if (!inner || (kMod && P.window > 0)) {
+          const int s = s0 + lane;
+          const bool live = s < S, paged = unsigned(lane < 16 ? ph0 : ph1) < unsigned(P.num_pages);
+          bool see = live && paged;
+          if (live && !paged) report(P.status, KVSEL_ERR_BAD_INDEX);
+          if (kMod && P.window > 0) {
+            const int p = mapped ? st.pos[lane] : s;
+            see = see && (pos_q - p < P.window || p < P.n_sink);
+          }
+          vis = __ballot_sync(0xffffffffu, see);
+          // what is not seen must not reach the product with p = 0 as NaN or infinity
+          if (!see) {
+            own = make_uint4(0, 0, 0, 0);
+            st.vs[lane] = own;
+          }
         }
         // the scales' running exponents
         const uint32_t sc[4] = {own.x & 0x7F80u, own.y & 0x7F80u, own.z & 0x7F80u, own.w & 0x7F80u};
@@ -694,6 +715,11 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     if (P.next_pos) P.next_pos[b] += 1;
   }
   if (chunk >= 0 && chunk * kQfSlots >= S) return;
+  if (chunk >= 0 && !P.probs) {   // a chunk that nobody sees adds nothing to the scores
+    const TileSet t = tiles_of(S, P.window, P.n_sink, mapped);
+    const int first = chunk * (kQfSlots / kQdTile), last = first + kQfSlots / kQdTile - 1;
+    if (first >= t.sink_tiles && last < t.win_tile) return;
+  }
 
   const int pre = __ldcg(P.tile_pre + b), tot = __ldcg(P.tile_pre + P.B);
   const TileSet ts = tiles_of(S, P.window, P.n_sink, mapped);
@@ -749,6 +775,28 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     return;
   }
 
+  const float* lg = P.logits + ((size_t)b * P.Hq + kvh * P.G) * P.max_len;
+  float* crow = P.cum ? P.cum + rowi * P.max_len : nullptr;
+  const int new_slot = P.new_kv[0] ? S - 1 : -1;
+  constexpr int kPer = kQfSlots / kQfThreads, kFirst = 4;
+  const int s0 = chunk * kQfSlots + tid;
+  bool use[kPer];
+  float sum[kPer], old[kPer], v[kFirst][kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int s = s0 + k * kQfThreads;
+    use[k] = s < S && ts.holds(s / kQdTile);
+    sum[k] = 0.f;
+    old[k] = crow && use[k] && s != new_slot ? __ldcg(crow + s) : 0.f;   // the appended slot starts from 0
+  }
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int h = 0; h < kFirst; ++h)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        v[h][k] = use[k] && h0 + h < P.G ? __ldcs(lg + (size_t)(h0 + h) * P.max_len + s0 + k * kQfThreads) : -INFINITY;
+  };
+  load(0);   // on their way while the statistics are joined
   // every head's maximum and 1 / sum: 16 threads a head, the first 4 partials of each read at once
   {
     const int head = tid >> 4, l16 = tid & 15;
@@ -781,36 +829,20 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     }
   }
   __syncthreads();
-  const float* lg = P.logits + ((size_t)b * P.Hq + kvh * P.G) * P.max_len;
-  float* crow = P.cum ? P.cum + rowi * P.max_len : nullptr;
-  const int new_slot = P.new_kv[0] ? S - 1 : -1;
-  constexpr int kPer = kQfSlots / kQfThreads;
-  const int s0 = chunk * kQfSlots + tid;
-  bool use[kPer];
-  float sum[kPer], old[kPer];
+#pragma unroll 1
+  for (int h0 = 0; h0 < P.G; h0 += kFirst) {
+    if (h0 > 0) load(h0);
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int s = s0 + k * kQfThreads;
-    use[k] = s < S && ts.holds(s / kQdTile);
-    sum[k] = 0.f;
-    old[k] = crow && use[k] && s != new_slot ? __ldcg(crow + s) : 0.f;   // the appended slot starts from 0
-  }
-#pragma unroll 4
-  for (int h = 0; h < P.G; ++h) {
-    float v[kPer];
+    for (int h = 0; h < kFirst; ++h) {
+      if (h0 + h >= P.G) break;
+      const float mh = s_m[h0 + h], ih = s_inv[h0 + h];
+      float* pr = P.probs ? P.probs + ((size_t)b * P.Hq + kvh * P.G + h0 + h) * P.max_len + s0 : nullptr;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) v[k] = use[k] ? __ldcs(lg + (size_t)h * P.max_len + s0 + k * kQfThreads) : -INFINITY;
-    const float mh = s_m[h], ih = s_inv[h];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      v[k] = ex2(v[k] - mh) * ih;
-      sum[k] += v[k];
-    }
-    if (P.probs) {
-      float* pr = P.probs + ((size_t)b * P.Hq + kvh * P.G + h) * P.max_len + s0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (s0 + k * kQfThreads < S) pr[k * kQfThreads] = v[k];
+      for (int k = 0; k < kPer; ++k) {
+        const float p = ex2(v[h][k] - mh) * ih;
+        sum[k] += p;
+        if (pr && s0 + k * kQfThreads < S) pr[k * kQfThreads] = p;
+      }
     }
   }
   if (crow) {
@@ -833,14 +865,14 @@ struct Decode4Ws {
   size_t eff_off, pre_off, ml_off, o_off, logits_off, total;
 };
 
-// CTAs of the main kernel: every co-resident slot.
-int decode4_ctas(int G) { return sm_count() * (G > 8 ? kQdCtasWide : kQdCtas); }
+// Warps of the main kernel: one CTA an SM.
+int decode4_warps(int G) { return sm_count() * (G > 8 ? kQdWarpsWide : kQdWarps); }
 
 // The workspace is sized for the largest grid the device could take; the
 // number of SMs is that of the current device.
-Decode4Ws decode4_layout(const kvsel_paged_kv4* kv, int batch, int max_len, bool own_logits, int ctas) {
+Decode4Ws decode4_layout(const kvsel_paged_kv4* kv, int batch, int max_len, bool own_logits, int warps) {
   const int G = kv->num_q_heads / kv->num_kv_heads;
-  const size_t parts = size_t(ctas) * kQdWarps + size_t(batch) * kv->num_kv_heads;
+  const size_t parts = size_t(warps) + size_t(batch) * kv->num_kv_heads;
   Decode4Ws w;
   w.eff_off = kStatusBytes;
   w.pre_off = align_up(w.eff_off + size_t(batch) * 4, 256);
@@ -865,13 +897,14 @@ kvsel_status check_shape(const std::string& fn, const kvsel_paged_kv4* kv) {
 }
 
 template <bool kWide, bool kMod>
-kvsel_status launch_main(const Decode4Params& P, int ctas, cudaStream_t st) {
+kvsel_status launch_main(const Decode4Params& P, cudaStream_t st) {
   auto* fn = &kv4_decode_kernel<kWide, kMod, kQdStages>;
-  const int smem = int(sizeof(QdStage)) * kQdStages * kQdWarps;
+  constexpr int kW = kWide ? kQdWarpsWide : kQdWarps;
+  const int smem = int(sizeof(QdStage)) * kQdStages * kW;
   if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(fn), smem); e != cudaSuccess)
     return cuda_fail(e, "kvsel_kv4_decode_attn (attribute)");
   trace_before("kv4_decode", st);
-  fn<<<ctas, kQdThreads, smem, st>>>(P);
+  fn<<<P.warps / kW, kW * 32, smem, st>>>(P);
   cudaError_t e = cudaGetLastError();
   trace_after(st);
   if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_decode_attn (launch)");
@@ -883,7 +916,7 @@ kvsel_status launch_main(const Decode4Params& P, int ctas, cudaStream_t st) {
 extern "C" size_t kvsel_kv4_decode_attn_workspace(const kvsel_paged_kv4* kv, int batch, int max_len, int with_probs,
                                                   int with_cum) {
   if (batch < 1 || batch > kQdMaxBatch || max_len < 1 || check_shape("", kv) != KVSEL_OK) return 0;
-  return decode4_layout(kv, batch, max_len, with_cum && !with_probs, decode4_ctas(kv->num_q_heads / kv->num_kv_heads)).total;
+  return decode4_layout(kv, batch, max_len, with_cum && !with_probs, decode4_warps(kv->num_q_heads / kv->num_kv_heads)).total;
 }
 
 extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const int32_t* block_table, int max_pages,
@@ -910,9 +943,9 @@ extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const i
     return fail(KVSEL_ERR_INVALID_ARG, fn + "need 0 <= softcap <= 1e30, window >= 0, n_sink >= 0");
   if (!workspace || !aligned(workspace, 256)) return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace is required");
   const int G = kv->num_q_heads / kv->num_kv_heads;
-  const int ctas = decode4_ctas(G);
+  const int warps = decode4_warps(G);
   const bool own_logits = h2o_cum && !probs;
-  const Decode4Ws L = decode4_layout(kv, batch, max_len, own_logits, ctas);
+  const Decode4Ws L = decode4_layout(kv, batch, max_len, own_logits, warps);
   if (ws_bytes < L.total) return fail(KVSEL_ERR_INVALID_ARG, fn + "workspace too small: need " + std::to_string(L.total));
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -952,10 +985,10 @@ extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const i
   P.num_pages = kv->num_pages;
   P.page_lg = 4 + page_shift_of(kv->page_size);
   P.out_bf16 = out_dtype == KVSEL_BF16;
-  P.warps = ctas * kQdWarps;
+  P.warps = warps;
   const bool modded = P.softcap > 0.f || P.slopes || P.window > 0;
-  kvsel_status s = G > 8 ? (modded ? launch_main<true, true>(P, ctas, st) : launch_main<true, false>(P, ctas, st))
-                         : (modded ? launch_main<false, true>(P, ctas, st) : launch_main<false, false>(P, ctas, st));
+  kvsel_status s = G > 8 ? (modded ? launch_main<true, true>(P, st) : launch_main<true, false>(P, st))
+                         : (modded ? launch_main<false, true>(P, st) : launch_main<false, false>(P, st));
   if (s != KVSEL_OK) return s;
 
   cudaLaunchAttribute attr[1];
