@@ -9,7 +9,7 @@
 //   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
 // evict: the select of h2o_evict.cu, then one cluster of 8 CTAs per
-//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 128 kept
+//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 112 kept
 //   rows in the cluster's shared memory, waits for the whole cluster and
 //   writes them to their new slots; kept lists are ascending, so keep[i] >= i
 //   and a round never writes a slot that a later round still reads, which lets
@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P
 // compaction
 // ---------------------------------------------------------------------------
 constexpr int kQcCluster = 8;
-constexpr int kQcRows = 128;     // kept rows a CTA stages per round
+constexpr int kQcRows = 112;     // kept rows a CTA stages per round; four CTAs an SM
+constexpr int kQcRounds = 8;     // rounds whose places are looked up together
 constexpr int kQcThreads = 256;
 constexpr int kQcUnits = 10;     // 16-byte units of a row: K codes 4, V codes 4, K and V scales
+constexpr uint32_t kQcNone = 0xFFFFFFFFu;
 
 struct Compact4Params {
   const int32_t* seq_lens;
@@ -253,16 +255,16 @@ struct Compact4Params {
   int Hkv, max_len, max_pages, num_pages, budget, page_lg;
 };
 
-struct Compact4Stage {
-  uint4 unit[kQcRows][kQcUnits];
-  long long src[kQcRows], dst[kQcRows];  // pool rows, -1: a bad table entry
-  float cum[kQcRows];
-  int32_t pos[kQcRows];
+struct Compact4Smem {
+  uint4 unit[2][kQcRows][kQcUnits];
+  uint32_t src[kQcRounds * kQcRows], dst[kQcRounds * kQcRows];  // pool rows, kQcNone: a bad table entry
+  float cum[kQcRounds * kQcRows];
+  int32_t pos[kQcRounds * kQcRows];
 };
 
 __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4Params P) {
   extern __shared__ __align__(16) uint8_t qc_smem[];
-  Compact4Stage* const stages = reinterpret_cast<Compact4Stage*>(qc_smem);   // two
+  Compact4Smem& sm = *reinterpret_cast<Compact4Smem*>(qc_smem);
   const int rank = blockIdx.x % kQcCluster, kvh = blockIdx.x / kQcCluster, b = blockIdx.y, tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept lists come from the select
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
@@ -278,13 +280,13 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
   float* crow = P.cum + rowi * P.max_len;
   int32_t* prow = P.pos_map ? P.pos_map + rowi * P.max_len : nullptr;
   const int page_mask = (1 << P.page_lg) - 1;
-  auto pool_row = [&](int slot) -> long long {
-    const int phys = bt[slot >> P.page_lg];
+  auto pool_row = [&](int slot) -> uint32_t {
+    const int phys = __ldg(bt + (slot >> P.page_lg));
     if (unsigned(phys) >= unsigned(P.num_pages)) {
       report(P.status, KVSEL_ERR_BAD_INDEX);
-      return -1;
+      return kQcNone;
     }
-    return (((long long)phys * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);
+    return ((uint32_t(phys) * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);   // < 2^31: checked on the host
   };
   // This CTA's rows of the round that starts at c0: an even share for every CTA of the cluster.
   auto share_of = [&](int c0, int& i0) {
@@ -293,56 +295,68 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
     i0 = c0 + rank * share;
     return max(0, min(share, left - rank * share));
   };
-  auto start = [&](int c0, Compact4Stage& sm) {   // its rows come into shared memory
-    int i0;
-    const int cnt = share_of(c0, i0);
-    for (int i = tid; i < cnt; i += kQcThreads) {
-      const int src = keep[i0 + i];
-      sm.src[i] = pool_row(src);
-      sm.dst[i] = pool_row(i0 + i);
-      sm.cum[i] = crow[src];
-      if (prow) sm.pos[i] = prow[src];
+  // thread t moves unit t % 10 of rows t / 10, t / 10 + 25, ... (250 of the 256 threads)
+  const int w = tid % kQcUnits, r0 = tid / kQcUnits;
+  constexpr int kStep = kQcThreads / kQcUnits;
+  uint8_t* const pool = w < 4 ? P.codes[0] + w * 16 : w < 8 ? P.codes[1] + (w - 4) * 16 : w == 8 ? P.scales[0] : P.scales[1];
+  const uint32_t bytes = w < 8 ? kQ4CodeBytes : kQ4ScaleBytes;
+  constexpr int kRound = kQcCluster * kQcRows;
+#pragma unroll 1
+  for (int c0 = P.first_move[rowi]; c0 < P.budget; c0 += kQcRounds * kRound) {
+    const int rounds = min(kQcRounds, (P.budget - c0 + kRound - 1) / kRound);
+    // where the rows of these rounds come from and go to; no source of a later row is written before
+    for (int x = tid; x < rounds * kQcRows; x += kQcThreads) {
+      const int k = x / kQcRows, i = x - k * kQcRows;
+      int i0;
+      if (i < share_of(c0 + k * kRound, i0)) {
+        const int src = keep[i0 + i];
+        sm.src[x] = pool_row(src);
+        sm.dst[x] = pool_row(i0 + i);
+        sm.cum[x] = crow[src];
+        if (prow) sm.pos[x] = prow[src];
+      }
     }
     __syncthreads();
-    for (int u = tid; u < cnt * kQcUnits; u += kQcThreads) {
-      const int i = u / kQcUnits, w = u - i * kQcUnits;
-      const long long row = sm.src[i];
-      if (row < 0) continue;
-      const uint8_t* from = w < 8 ? P.codes[w >> 2] + row * kQ4CodeBytes + (w & 3) * 16 : P.scales[w - 8] + row * kQ4ScaleBytes;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[i][w])), "l"(from) : "memory");
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  constexpr int kRound = kQcCluster * kQcRows;
-  int c0 = P.first_move[rowi], turn = 0;
-  if (c0 < P.budget) start(c0, stages[0]);
+    auto start = [&](int k) {   // round k's rows come into shared memory
+      int i0;
+      const int cnt = share_of(c0 + k * kRound, i0);
+      if (r0 < kStep)
+        for (int i = r0; i < cnt; i += kStep) {
+          const uint32_t row = sm.src[k * kQcRows + i];
+          if (row == kQcNone) continue;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[k & 1][i][w])), "l"(pool + (size_t)row * bytes) : "memory");
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    start(0);
 #pragma unroll 1
-  for (; c0 < P.budget; c0 += kRound, turn ^= 1) {
-    // the next round's rows are on their way while this one's are written: they lie behind every slot
-    // that this round writes
-    if (c0 + kRound < P.budget) {
-      start(c0 + kRound, stages[turn ^ 1]);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int k = 0; k < rounds; ++k) {
+      // the next round's rows are on their way while this one's are written: they lie behind every
+      // slot that this round writes
+      if (k + 1 < rounds) {
+        start(k + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      // all of the round's sources are in shared memory before any of its slots is written (what a CTA
+      // reads it has when it arrives, so the barrier need not order memory)
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+      int i0;
+      const int cnt = share_of(c0 + k * kRound, i0);
+      __syncthreads();   // the other threads' copies
+      if (r0 < kStep)
+        for (int i = r0; i < cnt; i += kStep) {
+          const uint32_t row = sm.dst[k * kQcRows + i];
+          if (row == kQcNone || sm.src[k * kQcRows + i] == kQcNone) continue;
+          *reinterpret_cast<uint4*>(pool + (size_t)row * bytes) = sm.unit[k & 1][i][w];
+        }
+      for (int i = tid; i < cnt; i += kQcThreads) {
+        crow[i0 + i] = sm.cum[k * kQcRows + i];
+        if (prow) prow[i0 + i] = sm.pos[k * kQcRows + i];
+      }
+      __syncthreads();   // the stage is free for the round after the next
     }
-    // all of the round's sources are in shared memory before any of its slots is written
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    Compact4Stage& sm = stages[turn];
-    int i0;
-    const int cnt = share_of(c0, i0);
-    for (int u = tid; u < cnt * kQcUnits; u += kQcThreads) {
-      const int i = u / kQcUnits, w = u - i * kQcUnits;
-      const long long row = sm.dst[i];
-      if (row < 0 || sm.src[i] < 0) continue;
-      uint8_t* to = w < 8 ? P.codes[w >> 2] + row * kQ4CodeBytes + (w & 3) * 16 : P.scales[w - 8] + row * kQ4ScaleBytes;
-      *reinterpret_cast<uint4*>(to) = sm.unit[i][w];
-    }
-    for (int i = tid; i < cnt; i += kQcThreads) {
-      crow[i0 + i] = sm.cum[i];
-      if (prow) prow[i0 + i] = sm.pos[i];
-    }
-    __syncthreads();   // the stage is free for the round after the next
   }
 }
 
@@ -362,6 +376,8 @@ kvsel_status check_kv4(const std::string& fn, const kvsel_paged_kv4* kv) {
     if (!aligned(p, 16)) return fail(KVSEL_ERR_INVALID_ARG, fn + "pools must be 16-byte aligned");
   if (page_shift_of(kv->page_size) < 0 || kv->head_dim != kQ4D)
     return fail(KVSEL_ERR_UNSUPPORTED, fn + "only head_dim 128 and page_size 16, 32, 64, 128 or 256 are implemented");
+  if ((long long)kv->num_pages * kv->num_kv_heads * kv->page_size >= (1ll << 31))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "num_pages * num_kv_heads * page_size must be below 2^31");
   return KVSEL_OK;
 }
 
@@ -545,14 +561,14 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   C.num_pages = kv->num_pages;
   C.budget = budget;
   C.page_lg = 4 + page_shift_of(kv->page_size);
-  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(2 * sizeof(Compact4Stage)));
+  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(sizeof(Compact4Smem)));
       e != cudaSuccess)
     return cuda_fail(e, "kvsel_kv4_evict (attribute)");
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(kv->num_kv_heads) * kQcCluster, batch);
   cfg.blockDim = dim3(kQcThreads);
-  cfg.dynamicSmemBytes = 2 * sizeof(Compact4Stage);
+  cfg.dynamicSmemBytes = sizeof(Compact4Smem);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

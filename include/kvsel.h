@@ -679,8 +679,9 @@ KVSEL_API kvsel_status kvsel_quest_decode(const kvsel_paged_kv* kv, const int32_
  *           row in the low half of byte i, value 2i + 1 in the high half
  *   scales  bf16 [num_pages][num_kv_heads][page_size][4][2]: {s, z} per group
  * 80 bytes a row instead of 256.  Pages, block table and lengths are those of
- * the bf16 cache; head_dim 128, page_size 16, 32, 64, 128 or 256 (else
- * KVSEL_ERR_UNSUPPORTED).  Every pool must be 16-byte aligned.
+ * the bf16 cache; head_dim 128, page_size 16, 32, 64, 128 or 256, num_pages *
+ * num_kv_heads * page_size < 2^31 (else KVSEL_ERR_UNSUPPORTED).  Every pool must
+ * be 16-byte aligned.
  */
 typedef struct kvsel_paged_kv4 {
   void* k_codes;
@@ -749,8 +750,8 @@ KVSEL_API kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t* 
  *   probs        entries j >= S_b are not written; keys that are not seen get 0.
  *   workspace    >= kvsel_kv4_decode_attn_workspace(...) bytes, zeroed before
  *                first use; calls that may overlap need workspaces of their own.
- * num_q_heads / num_kv_heads <= 16 and num_pages * num_kv_heads * page_size <
- * 2^31 (else UNSUPPORTED), batch <= 1024 (else INVALID_ARG).
+ * num_q_heads / num_kv_heads <= 16 (else UNSUPPORTED), batch <= 1024 (else
+ * INVALID_ARG).
  * A length that is negative or does not fit the table or max_len records
  * KVSEL_ERR_BAD_INDEX and nothing is computed for that sequence; keys on a page
  * outside the pool record it too and are not seen.  Two launches. */
