@@ -439,17 +439,22 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax: one thread a row
     const int t = warp >> 2;
-    // this tile's Q rows, 128-byte swizzled; rows past the end are zero
+    // this tile's Q rows, 128-byte swizzled; rows past the end are zero.  All 16 loads of a thread are
+    // under way before the first is stored (one by one they took 9 us of a CTA's start).
     if (t < tiles && n > 0) {
-#pragma unroll 4
+      uint4 v[16];
+      const int ch = tid & 15, r0 = (tid & 127) >> 4;
+#pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int r = (tid & 127) / 16 + 8 * k, ch = tid & 15, gr = row0 + t * kPfTileRows + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (gr < rows) {
-          const int i = gr / P.G, h = gr - i * P.G;
-          v = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
-        }
-        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+        const int gr = min(row0 + t * kPfTileRows + r0 + 8 * k, rows - 1);
+        const int i = gr / P.G, h = gr - i * P.G;
+        v[k] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int r = r0 + 8 * k;
+        if (row0 + t * kPfTileRows + r >= rows) v[k] = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[k];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q stores -> tensor-core reads
       mbar_arrive(smem_u32(&q_full[t]));
