@@ -238,6 +238,27 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const int off = __ldg(P.q_off + b), n_q = __ldg(P.q_off + b + 1) - off, S = __ldg(P.seq_lens + b);
   const int rows = n_q * P.G, row0 = s_tile * 2 * kPfTileRows;   // n_q * G < 2^31: checked on the host
 
+  // ---- Q: a thread's 16 pieces of its tile's rows, all under way at once (one by one they took 9 us of a
+  // CTA's start); rows past the end are zero
+  uint4 qv[16];
+  if (warp < 8) {
+    const int ch = tid & 15, first = row0 + (warp >> 2) * kPfTileRows + ((tid & 127) >> 4);
+    const int di = 8 / P.G, dh = 8 - di * P.G;
+    int i = first / P.G, h = first - i * P.G;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (first + 8 * k < rows)
+        qv[k] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
+      i += di;
+      h += dh;
+      if (h >= P.G) {
+        h -= P.G;
+        ++i;
+      }
+    }
+  }
+
   // ---- this thread's row: what it sees
   const int row = row0 + tid;
   const bool in = tid < 2 * kPfTileRows && row < rows;
@@ -439,22 +460,12 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax: one thread a row
     const int t = warp >> 2;
-    // this tile's Q rows, 128-byte swizzled; rows past the end are zero.  All 16 loads of a thread are
-    // under way before the first is stored (one by one they took 9 us of a CTA's start).
+    // this tile's Q rows, 128-byte swizzled
     if (t < tiles && n > 0) {
-      uint4 v[16];
-      const int ch = tid & 15, r0 = (tid & 127) >> 4;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int gr = min(row0 + t * kPfTileRows + r0 + 8 * k, rows - 1);
-        const int i = gr / P.G, h = gr - i * P.G;
-        v[k] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int r = r0 + 8 * k;
-        if (row0 + t * kPfTileRows + r >= rows) v[k] = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[k];
+        const int r = (tid & 127) / 16 + 8 * k, ch = tid & 15;
+        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = qv[k];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q stores -> tensor-core reads
       mbar_arrive(smem_u32(&q_full[t]));
