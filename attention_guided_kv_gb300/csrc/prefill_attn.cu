@@ -28,6 +28,8 @@
 // Keys at or past the sequence's length never matter whatever their pages
 // hold: their scores are masked and their V rows zeroed in shared memory (0
 // times NaN would be NaN).
+#include <type_traits>
+
 #include "common.cuh"
 #include "umma.cuh"
 
@@ -536,11 +538,23 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-slope2, fabsf(d - float(c)), x[c]);
         }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // Keys that are not seen score -infinity; scores that the polynomial has yet to see stay finite, they
+        // only leave the maximum and get p = 0 below.
+        const bool late = kCap && !kBias && poly;
         if (part) {
 #pragma unroll
-          for (int c = 0; c < kPfKeys; c += 2)
-            mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], (seen[c >> 5] >> (c & 31)) & 1u ? x[c] : -INFINITY,
-                                     (seen[c >> 5] >> (c & 31)) & 2u ? x[c + 1] : -INFINITY);
+          for (int c = 0; c < kPfKeys; c += 2) {
+            const float x0 = (seen[c >> 5] >> (c & 31)) & 1u ? x[c] : -INFINITY;
+            const float x1 = (seen[c >> 5] >> (c & 31)) & 2u ? x[c + 1] : -INFINITY;
+            mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x0, x1);
+            if (!kCap || kBias) {
+              x[c] = x0;
+              x[c + 1] = x1;
+            } else if (!late) {
+              x[c] = x0;
+              x[c + 1] = x1;
+            }
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < kPfKeys; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
@@ -568,40 +582,54 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
         const float use = m == -INFINITY ? 0.f : m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // Groups of 8 keys: the next group's arguments are computed between the exponentials of this one, so
+        // that the FMA pipe and the special-function unit work side by side.
+        constexpr int kGrp = 8;
+        auto argue = [&](auto late_p, int c0) {
+          if constexpr (decltype(late_p)::value) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t u[32];
-          if (kCap && !kBias && poly) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float &x0 = x[64 * hf + 2 * k], &x1 = x[64 * hf + 2 * k + 1];
+            for (int c = c0; c < c0 + kGrp; c += 2) {
               float z0, z1, y0, y1;
-              mul2(z0, z1, x0, x1, x0, x1);
+              mul2(z0, z1, x[c], x[c + 1], x[c], x[c + 1]);
               fma2(y0, y1, z0, z1, pc3, pc3, pc2, pc2);
               fma2(y0, y1, y0, y1, z0, z1, pc1, pc1);
               fma2(y0, y1, y0, y1, z0, z1, pc0, pc0);
-              fma2(x0, x1, x0, x1, y0, y1, -use, -use);
+              fma2(x[c], x[c + 1], x[c], x[c + 1], y0, y1, -use, -use);
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float &x0 = x[64 * hf + 2 * k], &x1 = x[64 * hf + 2 * k + 1];
-              if (kCap || kBias) add2(x0, x1, x0, x1, -use, -use);
-              else fma2(x0, x1, x0, x1, sc, sc, -use, -use);
+            for (int c = c0; c < c0 + kGrp; c += 2) {
+              if (kCap || kBias) add2(x[c], x[c + 1], x[c], x[c + 1], -use, -use);
+              else fma2(x[c], x[c + 1], x[c], x[c + 1], sc, sc, -use, -use);
             }
           }
+        };
+        auto raise = [&](auto late_p, auto mask_p) {
+          uint32_t u[32];
+          argue(late_p, 0);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int c = 64 * hf + 2 * k;
-            float e0 = pf_ex2(x[c]), e1 = pf_ex2(x[c + 1]);
-            if (part) {
-              e0 = (seen[c >> 5] >> (c & 31)) & 1u ? e0 : 0.f;
-              e1 = (seen[c >> 5] >> (c & 31)) & 2u ? e1 : 0.f;
+          for (int c0 = 0; c0 < kPfKeys; c0 += kGrp) {
+            if (c0 + kGrp < kPfKeys) argue(late_p, c0 + kGrp);
+#pragma unroll
+            for (int c = c0; c < c0 + kGrp; c += 2) {
+              float e0 = pf_ex2(x[c]), e1 = pf_ex2(x[c + 1]);
+              if constexpr (decltype(mask_p)::value) {
+                e0 = (seen[c >> 5] >> (c & 31)) & 1u ? e0 : 0.f;
+                e1 = (seen[c >> 5] >> (c & 31)) & 2u ? e1 : 0.f;
+              }
+              const int k = (c >> 1) & 1;
+              add2(sum[2 * k], sum[2 * k + 1], sum[2 * k], sum[2 * k + 1], e0, e1);
+              u[(c >> 1) & 31] = pack_bf16x2(e0, e1);
             }
-            add2(sum[2 * (k & 1)], sum[2 * (k & 1) + 1], sum[2 * (k & 1)], sum[2 * (k & 1) + 1], e0, e1);
-            u[k] = pack_bf16x2(e0, e1);
+            if ((c0 + kGrp) % 64 == 0) tmem_st32(s_addr + c0 / 64 * 32, u);
           }
-          tmem_st32(s_addr + 32 * hf, u);
+        };
+        if constexpr (kCap && !kBias) {
+          if (!late) raise(std::false_type{}, std::false_type{});
+          else if (part) raise(std::true_type{}, std::true_type{});
+          else raise(std::true_type{}, std::false_type{});
+        } else {
+          raise(std::false_type{}, std::false_type{});
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
