@@ -528,14 +528,17 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
               mul2(x[c], x[c + 1], x[c], x[c + 1], y0, y1);
             }
           }
-        } else if (kBias) {
-#pragma unroll
-          for (int c = 0; c < kPfKeys; c += 2) mul2(x[c], x[c + 1], x[c], x[c + 1], sc, sc);
         }
         if (kBias) {
-          const float d = float(pos - t0);
+          const float d = float(pos - t0), base = -slope2 * d, by = kCap ? 1.f : sc;
+          // without a prefix no key past the query is seen, and the distance has one sign
+          if (!P.prefix || __all_sync(0xffffffffu, pos - t0 >= kPfKeys - 1)) {
 #pragma unroll
-          for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(-slope2, fabsf(d - float(c)), x[c]);
+            for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(x[c], by, fmaf(slope2, float(c), base));
+          } else {
+#pragma unroll
+            for (int c = 0; c < kPfKeys; ++c) x[c] = fmaf(x[c], by, -slope2 * fabsf(d - float(c)));
+          }
         }
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         // Keys that are not seen score -infinity; scores that the polynomial has yet to see stay finite, they
