@@ -36,17 +36,20 @@ __device__ __forceinline__ float two_sum(float a, float b, float& err) {
 }
 
 // bf16 bits of (hi_v - lo_v) / 15 rounded to nearest even, 0 below 2^-100.
+// The product with 1 / 15 is within 2 units of its last place: only within 4 of
+// a border of bf16 can that matter, and there 15 times the border is compared
+// with the difference and its rounding error.
 __device__ __forceinline__ uint32_t q4_scale_bits(float hi_v, float lo_v) {
   float err;
   const float r = two_sum(hi_v, -lo_v, err);
-  const float q = __fdiv_rn(r, 15.0f);
-  const float rem = __fadd_rn(__fmaf_rn(-q, 15.0f, r), err);
-  uint32_t u = __float_as_uint(q);
-  if ((u & 0xFFFFu) == 0x8000u && rem != 0.0f) {
-    u = rem > 0.0f ? u + 1u : u - 1u;   // off the border, to the side of the exact quotient
+  const uint32_t u = __float_as_uint(r * (1.0f / 15.0f));
+  uint32_t b = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+  if ((u & 0xFFFFu) - 0x7FFCu <= 8u) {
+    const uint32_t down = u >> 16;
+    const float e = __fadd_rn(__fmaf_rn(-15.0f, __uint_as_float((down << 16) | 0x8000u), r), err);
+    b = e > 0.0f || (e == 0.0f && (down & 1u)) ? down + 1u : down;
   }
-  u = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-  return u < (27u << 7) ? 0u : u;       // 2^-100 has exponent field 27
+  return b < (27u << 7) ? 0u : b;       // 2^-100 has exponent field 27
 }
 
 // Packed bf16 minimum and maximum (a NaN wins), and the smaller magnitude (of
@@ -65,6 +68,18 @@ __device__ __forceinline__ uint32_t bf2_min_abs(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+// Two fp32 operations an instruction: (x, y) + c and (x, y) * b + (c, e).
+__device__ __forceinline__ void add2(float (&d)[2], float x, float y, float c) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(x), "f"(y), "f"(c));
+}
+__device__ __forceinline__ void fma2(float (&d)[2], float x, float y, float b, float c, float e) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(x), "f"(y), "f"(b), "f"(c), "f"(e));
 }
 __device__ __forceinline__ uint32_t swap_halves(uint32_t v) { return __funnelshift_l(v, v, 16); }
 
@@ -132,14 +147,17 @@ __device__ __forceinline__ uint32_t q4_group(const uint32_t (&raw)[NV / 2], uint
     const float inv_up = inv * (1.0f + 0x1p-20f);
     const uint32_t thr = __float_as_uint(-0.5f * s);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float x = i & 1 ? bf16hi_to_f32(raw[i / 2]) : bf16lo_to_f32(raw[i / 2]);
-      const float r = __fsub_rn(x, lo);
-      const float y = __fmaf_rn(r, inv_up, kMagic);
-      float n = __fsub_rn(y, kMagic);
-      const float d = __fmaf_rn(-n, s, r);
-      if (d <= __uint_as_float(thr | (~__float_as_uint(y) & 1u))) n = __fsub_rn(n, 1.0f);
-      v[i / 4] = __fmaf_rn(n, float(1 << (4 * (i & 3))), v[i / 4]);
+    for (int i = 0; i < NV; i += 2) {
+      float r[2], y[2], n[2], d[2];
+      add2(r, bf16lo_to_f32(raw[i / 2]), bf16hi_to_f32(raw[i / 2]), -lo);
+      fma2(y, r[0], r[1], inv_up, kMagic, kMagic);
+      add2(n, y[0], y[1], -kMagic);
+      fma2(d, n[0], n[1], -s, r[0], r[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (d[k] <= __uint_as_float(thr | (~__float_as_uint(y[k]) & 1u))) n[k] = __fsub_rn(n[k], 1.0f);
+        v[i / 4] = __fmaf_rn(n[k], float(1 << (4 * ((i + k) & 3))), v[i / 4]);
+      }
     }
   } else {
 #pragma unroll 1
