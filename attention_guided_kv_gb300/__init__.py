@@ -609,7 +609,7 @@ class _On:
 
 def _queue(stream, dev):
     """Handle of the given stream, or of the device's current one."""
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 def paged_kv4(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
