@@ -8,7 +8,8 @@
 // slot), and [S - window, S); evict the rest.
 //
 // select kernel, one 1024-thread CTA per (sequence, kv head): an exact
-//   top-k over a monotone uint32 image of the fp32 score (row_topk.cuh):
+//   top-k over a monotone uint32 image of the fp32 score (row_topk.cuh; rows
+//   of up to 4096 candidates are listed whole, see select_short):
 //   coalesced float4 loads into registers, a lower bound on the k-th key
 //   (the row's previous threshold, kept in the workspace, else a sample
 //   quantile), a radix select over the keys above that bound only, and an
@@ -116,6 +117,88 @@ __device__ __forceinline__ void list_radix(const uint32_t* ukey, uint32_t cnt, i
   need_eq = krem;
 }
 
+// The k largest of the cnt listed keys in shared memory (sm.rk.ukey, 0: not a
+// candidate; sm.upos: slots relative to lo; sm.m candidates between sm.minkey
+// and sm.rk.maxkey; the bitmaps clear), ties to the lower slot, through
+// put(i, slot) in ascending slot order.  Returns false, having written nothing,
+// if there are fewer than k (block-uniform).
+template <class Put>
+__device__ __forceinline__ bool select_listed(uint32_t cnt, int lo, int hi, int k, SelSmem& sm, uint32_t& T, Put put) {
+  const int tid = threadIdx.x, nw = (hi - lo + 31) >> 5;
+  if (sm.m < uint32_t(k)) return false;
+  uint32_t need_eq;
+  const uint32_t lo_key = sm.minkey, hi_key = sm.rk.maxkey;
+  if (lo_key == hi_key) {
+    T = lo_key;
+    need_eq = uint32_t(k);
+  } else {
+    list_radix(sm.rk.ukey, cnt, 31 - __clz(lo_key ^ hi_key), lo_key, uint32_t(k), sm.rk, T, need_eq);
+  }
+  for (uint32_t i = tid; i < cnt; i += kSelThreads) {
+    const uint32_t u = sm.rk.ukey[i];
+    if (u == 0u) continue;  // outside the candidate range
+    const int r = sm.upos[i];
+    if (u > T) atomicOr(&sm.bits[0][r >> 5], 1u << (r & 31));
+    else if (u == T) atomicOr(&sm.bits[1][r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
+  // ordered emission: thread t owns bitmap word t (32 slots)
+  const uint32_t wg = tid < nw ? sm.bits[0][tid] : 0u, we = tid < nw ? sm.bits[1][tid] : 0u;
+  uint32_t total;
+  const uint32_t ex = rk_block_excl_scan(uint32_t(__popc(wg)) | (uint32_t(__popc(we)) << 16), sm.rk.wtot[0], total);
+  const uint32_t g_before = ex & 0xFFFFu, e_before = ex >> 16;
+  const uint32_t take = need_eq > e_before ? min(uint32_t(__popc(we)), need_eq - e_before) : 0u;
+  uint32_t keepw = wg | lowest_bits(we, take);
+  uint32_t o = g_before + min(e_before, need_eq);
+  uint32_t* staged = sm.rk.ukey;
+  while (keepw) {
+    const int bit = __ffs(keepw) - 1;
+    keepw &= keepw - 1;
+    if (o < uint32_t(k)) staged[o] = uint32_t(tid * 32 + bit);
+    ++o;
+  }
+  __syncthreads();
+  for (int i = tid; i < k; i += kSelThreads) put(i, lo + int(staged[i]));
+  return true;
+}
+
+// Top-k of a short row's middle slots [lo, hi), at most kShortRow of them: all
+// of them are listed, so neither a bound nor a gathering pass is needed (8
+// rows of 1600 slots, events around the launch: 26 us with them, 14 without).
+constexpr int kShortRow = 4096;
+template <class Put>
+__device__ __forceinline__ bool select_short(const float* row, int lo, int hi, int k, SelSmem& sm, uint32_t& T, Put put) {
+  const int tid = threadIdx.x, lane = tid & 31, n = hi - lo, nw = (n + 31) >> 5;
+  if (tid == 0) {
+    sm.m = 0;
+    sm.rk.maxkey = 0;
+    sm.minkey = 0xFFFFFFFFu;
+  }
+  for (int i = tid; i < nw; i += kSelThreads) sm.bits[0][i] = sm.bits[1][i] = 0u;
+  __syncthreads();
+  uint32_t mx = 0, mn = 0xFFFFFFFFu, n_in = 0;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const uint32_t key = order_key(__ldcg(row + lo + i));
+    sm.rk.ukey[i] = key;
+    sm.upos[i] = i;
+    if (key) {
+      mx = max(mx, key);
+      mn = min(mn, key);
+      ++n_in;
+    }
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  n_in = __reduce_add_sync(0xffffffffu, n_in);
+  if (lane == 0) {
+    if (mx) atomicMax(&sm.rk.maxkey, mx);
+    atomicMin(&sm.minkey, mn);
+    atomicAdd(&sm.m, n_in);
+  }
+  __syncthreads();
+  return select_listed(uint32_t(n), lo, hi, k, sm, T, put);
+}
+
 // Top-k of the middle slots [lo, hi) from the candidate list that the decode
 // step collected (every slot whose score is >= the row's last threshold).
 // Usable when the list is fresh and holds at least k slots of [lo, hi): the
@@ -184,42 +267,7 @@ __device__ __forceinline__ bool select_from_list(const SelectParams& P, size_t r
     atomicAdd(&sm.m, n_in);
   }
   if (__syncthreads_or(bad)) return false;
-  const uint32_t m = sm.m;
-  if (m < uint32_t(k)) return false;
-  uint32_t need_eq;
-  const uint32_t lo_key = sm.minkey, hi_key = sm.rk.maxkey;
-  if (lo_key == hi_key) {
-    T = lo_key;
-    need_eq = uint32_t(k);
-  } else {
-    list_radix(sm.rk.ukey, cnt, 31 - __clz(lo_key ^ hi_key), lo_key, uint32_t(k), sm.rk, T, need_eq);
-  }
-  for (uint32_t i = tid; i < cnt; i += kSelThreads) {
-    const uint32_t u = sm.rk.ukey[i];
-    if (u == 0u) continue;  // outside the candidate range
-    const int r = sm.upos[i];
-    if (u > T) atomicOr(&sm.bits[0][r >> 5], 1u << (r & 31));
-    else if (u == T) atomicOr(&sm.bits[1][r >> 5], 1u << (r & 31));
-  }
-  __syncthreads();
-  // ordered emission: thread t owns bitmap word t (32 slots)
-  const uint32_t wg = tid < nw ? sm.bits[0][tid] : 0u, we = tid < nw ? sm.bits[1][tid] : 0u;
-  uint32_t total;
-  const uint32_t ex = rk_block_excl_scan(uint32_t(__popc(wg)) | (uint32_t(__popc(we)) << 16), sm.rk.wtot[0], total);
-  const uint32_t g_before = ex & 0xFFFFu, e_before = ex >> 16;
-  const uint32_t take = need_eq > e_before ? min(uint32_t(__popc(we)), need_eq - e_before) : 0u;
-  uint32_t keepw = wg | lowest_bits(we, take);
-  uint32_t o = g_before + min(e_before, need_eq);
-  uint32_t* staged = sm.rk.ukey;
-  while (keepw) {
-    const int bit = __ffs(keepw) - 1;
-    keepw &= keepw - 1;
-    if (o < uint32_t(k)) staged[o] = uint32_t(tid * 32 + bit);
-    ++o;
-  }
-  __syncthreads();
-  for (int i = tid; i < k; i += kSelThreads) put(i, lo + int(staged[i]));
-  return true;
+  return select_listed(cnt, lo, hi, k, sm, T, put);
 }
 
 // Per (sequence, kv head) row: the sinks, the k heaviest middle slots
@@ -286,6 +334,8 @@ __global__ void __launch_bounds__(kSelThreads) h2o_select_kernel(const SelectPar
     if (hk != 0u && cnt >= uint32_t(k) && cnt <= uint32_t(kLinkCap) && hi - lo <= 32 * kListWords)
       done = select_from_list(P, rowi, row, cnt, lo, hi, k, sm, T,
                               [&](int i, int slot) { put(P.n_sink + i, slot); });
+    if (!done && hi - lo <= kShortRow)
+      done = select_short(row, lo, hi, k, sm, T, [&](int i, int slot) { put(P.n_sink + i, slot); });
     if (!done) {
       const int a = P.n_sink & ~3;  // float4-aligned start of the candidate run
       const float* base = row + a;

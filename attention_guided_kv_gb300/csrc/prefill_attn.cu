@@ -842,9 +842,9 @@ extern "C" kvsel_status kvsel_prefill_attn(const kvsel_paged_kv* kv, const int32
   P.page_lg = 4 + page_shift_of(kv->page_size);
   P.total_q = total_q;
   P.out_bf16 = out_dtype == KVSEL_BF16;
-  // at least four key tiles a part, by the most that the table can hold
+  // at least two key tiles a part, by the most that the table can hold
   const long long key_tiles = ((long long)max_pages * kv->page_size + kPfKeys - 1) / kPfKeys;
-  P.splits = int(key_tiles / 4 < L.splits ? (key_tiles / 4 > 1 ? key_tiles / 4 : 1) : L.splits);
+  P.splits = int(key_tiles / 2 < L.splits ? (key_tiles / 2 > 1 ? key_tiles / 2 : 1) : L.splits);
   auto* fnp = softcap > 0.f ? (slopes ? &prefill_attn_kernel<true, true> : &prefill_attn_kernel<true, false>)
                             : (slopes ? &prefill_attn_kernel<false, true> : &prefill_attn_kernel<false, false>);
   if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(fnp), kPfSmem); e != cudaSuccess)
