@@ -578,6 +578,8 @@ def _required(t, dtype, shape, dev, name):
 
 def _scratch(workspace, dev):
     """(pointer, bytes) of a workspace of any type."""
+    if workspace is None:
+        raise ValueError("workspace is required")
     return _required(workspace, workspace.dtype, workspace.shape, dev, "workspace"), workspace.nbytes
 
 

@@ -932,6 +932,8 @@ extern "C" kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const i
   if (!block_table || !seq_lens || !q || !out || max_pages < 1 || max_len < 1)
     return fail(KVSEL_ERR_INVALID_ARG, fn + "block_table, seq_lens, q, out required; max_pages, max_len >= 1");
   if (batch < 1 || batch > kQdMaxBatch) return fail(KVSEL_ERR_INVALID_ARG, fn + "1 <= batch <= 1024");
+  if ((long long)batch * ((max_len + kQdTile - 1ll) / kQdTile) >= (1ll << 31))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "batch * max_len must be below 2^36");
   if (kv->num_kv_heads > 65535) return fail(KVSEL_ERR_UNSUPPORTED, fn + "at most 65535 kv heads");
   if ((k_new == nullptr) != (v_new == nullptr)) return fail(KVSEL_ERR_INVALID_ARG, fn + "k_new and v_new go together");
   if (pos_map && k_new && !next_pos) return fail(KVSEL_ERR_INVALID_ARG, fn + "pos_map needs next_pos when a token is appended");

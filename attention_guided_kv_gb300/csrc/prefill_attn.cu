@@ -203,7 +203,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (warp == 0) {
     int before = 0, found = -1, tile = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < P.B && found < 0; b0 += 32) {
+    for (int b0 = 0; b0 < P.B && (found < 0 || blockIdx.x == 0); b0 += 32) {   // the first CTA reports on all
       const int b = b0 + lane;
       int nt = 0;
       if (b < P.B) {
@@ -220,7 +220,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       const bool mine = want >= before + x - nt && want < before + x;
       const uint32_t who = __ballot_sync(0xffffffffu, mine);
-      if (who) {
+      if (who && found < 0) {
         const int src = __ffs(who) - 1;
         found = b0 + src;
         tile = __shfl_sync(0xffffffffu, before + x - 1 - want, src);

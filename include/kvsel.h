@@ -24,9 +24,10 @@
  *  - CUDA graphs: calls of kvsel_decode_attn, kvsel_h2o_evict,
  *    kvsel_snapkv_select and kvsel_block_priority (with their input and
  *    output copies) have been captured and replayed, the first two with
- *    results identical to the same calls made eagerly; kvsel_sparse_decode
- *    must not be captured (see its notes); the other entry points have not
- *    been tried in a graph.
+ *    results identical to the same calls made eagerly, as have been
+ *    kvsel_kv4_append, kvsel_kv4_decode_attn, kvsel_kv4_evict and
+ *    kvsel_prefill_attn; kvsel_sparse_decode must not be captured (see its
+ *    notes); the other entry points have not been tried in a graph.
  *  - No C++ exception crosses this interface.
  *
  * Paged KV layout (the paged cache of "From sliding window to
@@ -750,8 +751,8 @@ KVSEL_API kvsel_status kvsel_kv4_read(const kvsel_paged_kv4* kv, const int32_t* 
  *   probs        entries j >= S_b are not written; keys that are not seen get 0.
  *   workspace    >= kvsel_kv4_decode_attn_workspace(...) bytes, zeroed before
  *                first use; calls that may overlap need workspaces of their own.
- * num_q_heads / num_kv_heads <= 16 (else UNSUPPORTED), batch <= 1024 (else
- * INVALID_ARG).
+ * num_q_heads / num_kv_heads <= 16 and batch * max_len < 2^36 (else
+ * UNSUPPORTED), batch <= 1024 (else INVALID_ARG).
  * A length that is negative or does not fit the table or max_len records
  * KVSEL_ERR_BAD_INDEX and nothing is computed for that sequence; keys on a page
  * outside the pool record it too and are not seen.  Two launches. */

@@ -28,7 +28,7 @@ def _kv(**kw):
 
 BAD_KV = [(dict(k_codes=None), INV), (dict(v_scales=None), INV), (dict(k_scales=8), INV), (dict(v_codes=24), INV),
           (dict(num_pages=0), INV), (dict(num_kv_heads=0), INV), (dict(head_dim=64), UNS), (dict(page_size=8), UNS),
-          (dict(page_size=48), UNS), (dict(page_size=512), UNS)]
+          (dict(page_size=48), UNS), (dict(page_size=512), UNS), (dict(num_pages=1 << 24), UNS)]
 
 
 def _append(lib, kv=None, **over):
@@ -98,6 +98,7 @@ def test_decode(lib):
     assert _decode(lib, _kv(num_q_heads=12)) == INV                # not a multiple of 8
     assert _decode(lib, _kv(num_q_heads=0)) == INV
     assert _decode(lib, _kv(num_q_heads=136)) == UNS               # 17 q heads per kv head
+    assert _decode(lib, batch=1024, max_len=1 << 26) == UNS        # tiles beyond 32 bits
     for mod in (K.ScoreMod(softcap=-1.0), K.ScoreMod(softcap=math.nan), K.ScoreMod(softcap=math.inf),
                 K.ScoreMod(window=-1), K.ScoreMod(window=4, n_sink=-1)):
         assert _decode(lib, mod=mod) == INV

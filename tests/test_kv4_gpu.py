@@ -357,6 +357,31 @@ def test_decode_modified_scores(kw, G):
     _decode_case(G, 2, 16, [400, 77, 33, 1], spoil=True, seed=5, cap_extra=3, **kw)
 
 
+def test_append_is_the_format_on_many_rows():
+    """Scales and codes next to their borders: quarter steps, a wide spread of magnitudes, plain normals."""
+    rng = np.random.default_rng(77)
+    rows, Hkv = 96, 2
+    for kind in ("grid", "wide", "normal"):
+        c = Cache(rng, 1, Hkv, Hkv, 32, rows)
+        x = _inputs(rng, kind, rows * Hkv)
+        if kind == "normal":      # maxima that are 15 bf16 borders above the minimum
+            x = x.view(rows, Hkv, 4, 32).clone()
+            lo = x.amin(-1).float()
+            step = torch.from_numpy(2.0 ** rng.integers(-6, 3, lo.shape) * (1 + (2 * rng.integers(0, 128, lo.shape) + 1) / 256.0))
+            x[..., 0] = (lo + 15 * step.float()).bfloat16()
+            x = x.view(rows * Hkv, D)
+        xd = x.view(rows, Hkv, D).cuda()
+        seq, ws = ints([0]), K.workspace(512)
+        K.kvsel_kv4_append(c.kv, c.table, seq, ints([0, rows]), xd, xd, ws)
+        assert K.read_status(ws) == 0
+        want = kv4.quantise_rows(x.double().numpy())
+        for h in range(Hkv):
+            for side in range(2):
+                codes, s, z = c.rows(0, h, rows, side)
+                assert np.array_equal(s, want[1][h::Hkv]) and np.array_equal(z, want[2][h::Hkv]), kind
+                assert np.array_equal(codes, want[0][h::Hkv]), kind
+
+
 @pytest.mark.parametrize("probs,cum", [(True, False), (False, True), (False, False)])
 def test_decode_outputs_are_optional(probs, cum):
     _decode_case(8, 2, 16, [130, 64], probs=probs, cum=cum, seed=3)
@@ -632,6 +657,8 @@ def test_binding_checks_shapes_and_devices():
                 dict(slopes=torch.zeros(2, device="cuda")), dict(next_pos=ints([1])), dict(k_new=q[:, :2].contiguous()[:1])):
         with pytest.raises(ValueError):
             K.kvsel_kv4_decode_attn(c.kv, c.table, seq, q, out, ws, **bad)
+    with pytest.raises(ValueError):
+        K.kvsel_kv4_decode_attn(c.kv, c.table, seq, q, out, None, **ok)
     with pytest.raises(ValueError):
         K.paged_kv4(c.codes[0], c.codes[1][:1], c.scales[0], c.scales[1], 4)
     with pytest.raises(ValueError):

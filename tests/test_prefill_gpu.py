@@ -197,6 +197,13 @@ def test_reports_what_does_not_fit():
         assert bool((out[3:6] == 7.0).all()) and torch.equal(out[:3], good[:3]) and torch.equal(out[6:], good[6:])
     assert run([20, 20, 20], [0, 3, 6, 10])[0] == K.KVSEL_ERR_BAD_INDEX
     assert run([20, 20, 20], [-1, 3, 6, 9])[0] == K.KVSEL_ERR_BAD_INDEX
+    many = torch.full((18, 2, D), 7.0, device="cuda")    # a bad length far behind the first CTA's sequence
+    lens = [20] * 36
+    lens[35] = 40
+    ws2 = K.workspace(1 << 20)
+    K.kvsel_prefill_attn(kv, table[:1].expand(36, 2).contiguous(), ints(lens), q.repeat(2, 1, 1), ints([0] * 2 + list(range(1, 18)) + [18] * 18),
+                         many, ws2)
+    assert K.read_status(ws2) == K.KVSEL_ERR_BAD_INDEX
     bad = table.clone()
     bad[1, 0] = 10 ** 6
     st, out = run([20, 20, 20], [0, 3, 6, 9], bad)
