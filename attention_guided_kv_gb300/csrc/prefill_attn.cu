@@ -374,12 +374,7 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       y = y_next;
     }
-    if (dead) {   // the copies in flight land before the shared memory goes away (a bounded wait)
-      for (int s = 0; s < kPfStages; ++s) {
-        for (int w = 0; w < 64; ++w) mbar_try_wait(smem_u32(&k_full[s]), 0);
-        for (int w = 0; w < 64; ++w) mbar_try_wait(smem_u32(&v_full[s]), 0);
-      }
-    }
+    // (a wait that ran out lasted for seconds after the last copy was started: none is in flight then)
   } else if (warp == 9) {
     // ---- MMA issuer
     const uint32_t id_qk = umma_idesc_bf16_f32(128, kPfKeys), id_pv = umma_idesc_bf16_f32(128, kPfD) | (1u << 16);
