@@ -240,18 +240,18 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   const int off = __ldg(P.q_off + b), n_q = __ldg(P.q_off + b + 1) - off, S = __ldg(P.seq_lens + b);
   const int rows = n_q * P.G, row0 = s_tile * 2 * kPfTileRows;   // n_q * G < 2^31: checked on the host
 
-  // ---- Q: a thread's 16 pieces of its tile's rows, all under way at once (one by one they took 9 us of a
-  // CTA's start); rows past the end are zero
-  uint4 qv[16];
-  if (warp < 8) {
-    const int ch = tid & 15, first = row0 + (warp >> 2) * kPfTileRows + ((tid & 127) >> 4);
+  // ---- Q into shared memory, 128-byte swizzled, without waiting; rows past the end are zero
+  const int tiles = rows - row0 > kPfTileRows ? 2 : 1;
+  if (warp < 8 && (warp >> 2) < tiles) {
+    const int t = warp >> 2, ch = tid & 15, r0 = (tid & 127) >> 4, first = row0 + t * kPfTileRows + r0;
     const int di = 8 / P.G, dh = 8 - di * P.G;
     int i = first / P.G, h = first - i * P.G;
-#pragma unroll
+    const uint32_t to = smem_u32(sQ) + t * kPfTileBytes + (ch >> 3) * kPfSlab + r0 * 128 + (((ch & 7) ^ r0) << 4);
+#pragma unroll 4
     for (int k = 0; k < 16; ++k) {
-      qv[k] = make_uint4(0, 0, 0, 0);
-      if (first + 8 * k < rows)
-        qv[k] = __ldg(reinterpret_cast<const uint4*>(P.q + ((size_t)(off + i) * P.Hq + kvh * P.G + h) * kPfD) + ch);
+      const bool have = first + 8 * k < rows;
+      const __nv_bfloat16* from = P.q + ((size_t)(off + (have ? i : 0)) * P.Hq + kvh * P.G + (have ? h : 0)) * kPfD + ch * 8;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * 1024), "l"(from), "r"(have ? 16 : 0) : "memory");
       i += di;
       h += dh;
       if (h >= P.G) {
@@ -287,7 +287,6 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       atomicMax(&s_rng[3], b_hi);
     }
   }
-  const int tiles = rows - row0 > kPfTileRows ? 2 : 1;
   if (tid == 0) {
     for (int s = 0; s < kPfStages; ++s) {
       mbar_init(smem_u32(&k_full[s]), 1);
@@ -457,13 +456,8 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax: one thread a row
     const int t = warp >> 2;
-    // this tile's Q rows, 128-byte swizzled
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (t < tiles && n > 0) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int r = (tid & 127) / 16 + 8 * k, ch = tid & 15;
-        *reinterpret_cast<uint4*>(sQ + t * kPfTileBytes + (ch >> 3) * kPfSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = qv[k];
-      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // Q stores -> tensor-core reads
       mbar_arrive(smem_u32(&q_full[t]));
     }
@@ -634,40 +628,70 @@ prefill_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[t]));
       }
-      if (n > 0 && ok) {
-        ok = mbar_wait(smem_u32(&o_full[t]), 0, P.status);
-        ok = __all_sync(0xffffffffu, ok);
-      }
+      if (n > 0 && ok) ok = mbar_wait(smem_u32(&o_full[t]), 0, P.status);
+      __syncwarp();
       tc_fence_after();
-      const size_t at = (size_t)(off + qi) * P.Hq + head;
-      if (ok) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;      // nothing seen: 0
+      // The output goes through this tile's Q rows (every product with them is done), so that 16 lanes store a
+      // row's 256 bytes together; stored by the row's own thread, 16 bytes of 32 rows at a time, it took 3 us.
+      // All four warps come here, and agree on whether every wait was fine.
+      uint32_t all;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                   : "=r"(all)
+                   : "r"(1 + t), "r"(uint32_t(ok))
+                   : "memory");
+      if (all) {
+        const float inv = l == 0.f || P.splits > 1 ? 1.f : 1.f / l;
+        const bool wide = P.splits > 1 || !P.out_bf16;   // fp32: two passes of 64 dims
+        uint8_t* stage = sQ + t * kPfTileBytes;
+        const int r = tid & 127, ch = tid & 15, r0 = r >> 4, first = row0 + t * kPfTileRows + r0;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          if (n > 0) tmem_ld32(o_addr + 32 * c, o);
-          if (l == 0.f || n == 0) {
+        for (int pass = 0; pass < (wide ? 2 : 1); ++pass) {
+          if (pass) asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+#pragma unroll 1
+          for (int c = 0; c < (wide ? 2 : 4); ++c) {
+            float o[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            if (n > 0) tmem_ld32(o_addr + 64 * pass + 32 * c, o);
+            if (l == 0.f) {              // nothing seen: 0
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            }
+            if (wide) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float4*>(stage + r * 256 + (((8 * c + k) ^ (r & 15)) << 4)) =
+                    make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(stage + r * 256 + (((4 * c + k) ^ (r & 15)) << 4)) =
+                    make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                               pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            }
           }
-          if (!in) continue;
-          if (P.splits > 1) {
-            float4* to = reinterpret_cast<float4*>(P.part_o + ((size_t)split * P.total_q * P.Hq + at) * kPfD + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else if (P.out_bf16) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.out) + at * kPfD + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              to[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                 pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-          } else {
-            float4* to = reinterpret_cast<float4*>(static_cast<float*>(P.out) + at * kPfD + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              to[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+          uint8_t* base = P.splits > 1 ? reinterpret_cast<uint8_t*>(P.part_o + (size_t)split * P.total_q * P.Hq * kPfD)
+                                       : static_cast<uint8_t*>(P.out);
+          const int di = 8 / P.G, dh = 8 - di * P.G;
+          int i = first / P.G, h = first - i * P.G;
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {
+            const int rr = r0 + 8 * k;
+            if (first + 8 * k < rows) {
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 256 + ((ch ^ (rr & 15)) << 4));
+              const size_t row_at = (size_t)(off + i) * P.Hq + kvh * P.G + h;
+              *reinterpret_cast<uint4*>(base + row_at * (wide ? 512 : 256) + pass * 256 + ch * 16) = v;
+            }
+            i += di;
+            h += dh;
+            if (h >= P.G) {
+              h -= P.G;
+              ++i;
+            }
           }
         }
+        const size_t at = (size_t)(off + qi) * P.Hq + head;
         if (in && P.splits > 1) P.part_ml[(size_t)split * P.total_q * P.Hq + at] = make_float2(m, l);
         else if (in && P.lse) P.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kPfLn2;
       }
