@@ -1,5 +1,5 @@
 // The H2O select and truncate launches, shared by the evictions of the bf16
-// and the 4-bit cache (h2o_evict.cu).
+// and the 4-bit cache (h2o_evict.cu, h2o_select_long.cu).
 #pragma once
 
 #include "common.cuh"
@@ -19,6 +19,11 @@ struct H2OSelectArgs {
   int batch, num_kv_heads, max_len, budget, n_sink, window;
 };
 kvsel_status launch_h2o_select(const char* fn, const H2OSelectArgs& a, cudaStream_t st);
+
+// The same for long rows, each spread over many CTAs (h2o_select_long.cu); rows
+// = batch * num_kv_heads at most 65535, scratch of h2o_long_bytes(rows).
+size_t h2o_long_bytes(int rows);
+kvsel_status launch_h2o_select_long(const char* fn, const H2OSelectArgs& a, void* scratch, cudaStream_t st);
 
 struct H2OTruncateArgs {
   int32_t* seq_lens;

@@ -8,14 +8,15 @@
 //   read twice and every store is part of a full 64-byte row: 512 bytes read
 //   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
-// evict: the select of h2o_evict.cu, then one cluster of 8 CTAs per
-//   (sequence, kv head) moves the kept rows.  A round stages up to 8 x 112 kept
-//   rows in the cluster's shared memory, waits for the whole cluster and
-//   writes them to their new slots; kept lists are ascending, so keep[i] >= i
-//   and a round never writes a slot that a later round still reads, which lets
-//   the next round's rows load meanwhile.  One cluster barrier a round is the
-//   only ordering; one CTA per (sequence, kv head), as the bf16 cache's
-//   compaction has it, leaves most SMs idle at 64 of them.
+// evict: the select of h2o_evict.cu, then the kept rows move in chunks of 224,
+//   claimed by a persistent grid in order.  A chunk comes into shared memory,
+//   says that it has been read, waits until all chunks before it of its
+//   (sequence, kv head) have been read, and is written to its new slots: kept
+//   lists ascend, so keep[i] >= i and only chunks before it can have sources
+//   there.  Every SM works whether there are 64 rows of 6.5K kept slots or
+//   one of 300K; one CTA per (sequence, kv head), as the bf16 cache's compaction
+//   has it, leaves most of them idle, and a cluster of 8 per (sequence, kv head)
+//   in lock-step rounds took 41 us at 64 x 6.5K and 1 us per 896 rows of one.
 #include "common.cuh"
 #include "h2o_select.cuh"
 #include "kv4.cuh"
@@ -235,12 +236,12 @@ __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P
 // ---------------------------------------------------------------------------
 // compaction
 // ---------------------------------------------------------------------------
-constexpr int kQcCluster = 8;
-constexpr int kQcRows = 112;     // kept rows a CTA stages per round; four CTAs an SM
-constexpr int kQcRounds = 8;     // rounds whose places are looked up together
+constexpr int kQcRows = 224;     // kept rows of a chunk; four CTAs an SM
+constexpr int kQcCtas = 4;
 constexpr int kQcThreads = 256;
 constexpr int kQcUnits = 10;     // 16-byte units of a row: K codes 4, V codes 4, K and V scales
 constexpr uint32_t kQcNone = 0xFFFFFFFFu;
+constexpr unsigned kQcSpins = 1u << 22;  // polls of the chunks before, each a short sleep: seconds
 
 struct Compact4Params {
   const int32_t* seq_lens;
@@ -252,111 +253,118 @@ struct Compact4Params {
   float* cum;
   int32_t* pos_map;
   int* status;
-  int Hkv, max_len, max_pages, num_pages, budget, page_lg;
+  // workspace, zero when the kernel starts: chunks claimed, per (sequence, kv head) the chunks that are
+  // known to have been read from the first on, and a word per chunk that says it has been read
+  uint32_t* ticket;
+  uint32_t* prefix;
+  uint32_t* read;
+  int batch, Hkv, max_len, max_pages, num_pages, budget, page_lg, chunks;
 };
 
 struct Compact4Smem {
-  uint4 unit[2][kQcRows][kQcUnits];
-  uint32_t src[kQcRounds * kQcRows], dst[kQcRounds * kQcRows];  // pool rows, kQcNone: a bad table entry
-  float cum[kQcRounds * kQcRows];
-  int32_t pos[kQcRounds * kQcRows];
+  uint4 unit[kQcRows][kQcUnits];
+  uint32_t src[kQcRows], dst[kQcRows];  // pool rows, kQcNone: a bad table entry
+  float cum[kQcRows];
+  int32_t pos[kQcRows];
+  uint32_t ticket;
 };
 
 __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4Params P) {
   extern __shared__ __align__(16) uint8_t qc_smem[];
   Compact4Smem& sm = *reinterpret_cast<Compact4Smem*>(qc_smem);
-  const int rank = blockIdx.x % kQcCluster, kvh = blockIdx.x / kQcCluster, b = blockIdx.y, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept lists come from the select
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
-  const int S = P.seq_lens[b];
-  if (S <= P.budget) return;  // the same for the whole cluster, as below
-  if (S > P.max_len || (long long)S > ((long long)P.max_pages << P.page_lg)) {
-    if (tid == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
-    return;
-  }
-  const size_t rowi = size_t(b) * P.Hkv + kvh;
-  const int32_t* keep = P.keep_slots + rowi * P.budget;
-  const int32_t* bt = P.block_table + size_t(b) * P.max_pages;
-  float* crow = P.cum + rowi * P.max_len;
-  int32_t* prow = P.pos_map ? P.pos_map + rowi * P.max_len : nullptr;
   const int page_mask = (1 << P.page_lg) - 1;
-  auto pool_row = [&](int slot) -> uint32_t {
-    const int phys = __ldg(bt + (slot >> P.page_lg));
-    if (unsigned(phys) >= unsigned(P.num_pages)) {
-      report(P.status, KVSEL_ERR_BAD_INDEX);
-      return kQcNone;
-    }
-    return ((uint32_t(phys) * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);   // < 2^31: checked on the host
-  };
-  // This CTA's rows of the round that starts at c0: an even share for every CTA of the cluster.
-  auto share_of = [&](int c0, int& i0) {
-    const int left = min(kQcCluster * kQcRows, P.budget - c0);
-    const int share = (left + kQcCluster - 1) / kQcCluster;
-    i0 = c0 + rank * share;
-    return max(0, min(share, left - rank * share));
-  };
+  const uint32_t pairs = uint32_t(P.batch) * P.Hkv, total = pairs * P.chunks;   // < 2^31: checked on the host
   // thread t moves unit t % 10 of rows t / 10, t / 10 + 25, ... (250 of the 256 threads)
   const int w = tid % kQcUnits, r0 = tid / kQcUnits;
   constexpr int kStep = kQcThreads / kQcUnits;
   uint8_t* const pool = w < 4 ? P.codes[0] + w * 16 : w < 8 ? P.codes[1] + (w - 4) * 16 : w == 8 ? P.scales[0] : P.scales[1];
   const uint32_t bytes = w < 8 ? kQ4CodeBytes : kQ4ScaleBytes;
-  constexpr int kRound = kQcCluster * kQcRows;
+  const unsigned limit = spin_limit(P.status, kQcSpins);
 #pragma unroll 1
-  for (int c0 = P.first_move[rowi]; c0 < P.budget; c0 += kQcRounds * kRound) {
-    const int rounds = min(kQcRounds, (P.budget - c0 + kRound - 1) / kRound);
-    // where the rows of these rounds come from and go to; no source of a later row is written before
-    for (int x = tid; x < rounds * kQcRows; x += kQcThreads) {
-      const int k = x / kQcRows, i = x - k * kQcRows;
-      int i0;
-      if (i < share_of(c0 + k * kRound, i0)) {
-        const int src = keep[i0 + i];
-        sm.src[x] = pool_row(src);
-        sm.dst[x] = pool_row(i0 + i);
-        sm.cum[x] = crow[src];
-        if (prow) sm.pos[x] = prow[src];
+  while (true) {
+    if (tid == 0) sm.ticket = atomicAdd(P.ticket, 1u);
+    __syncthreads();
+    const uint32_t ticket = sm.ticket;
+    if (ticket >= total) break;
+    // all rows' first chunks, then their second ones, ...
+    const uint32_t pair = ticket % pairs, k = ticket / pairs;
+    const int b = int(pair / P.Hkv), kvh = int(pair - uint32_t(b) * P.Hkv);
+    const int S = P.seq_lens[b];
+    const int i0 = S > P.budget ? P.first_move[pair] + int(k) * kQcRows : P.budget;
+    const bool fits = S <= P.max_len && (long long)S <= ((long long)P.max_pages << P.page_lg);
+    if (i0 >= P.budget || !fits) {   // nothing to move
+      if (!fits && k == 0 && tid == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+      __syncthreads();
+      continue;
+    }
+    const int cnt = min(kQcRows, P.budget - i0);
+    const int32_t* keep = P.keep_slots + size_t(pair) * P.budget + i0;
+    const int32_t* bt = P.block_table + size_t(b) * P.max_pages;
+    float* crow = P.cum + size_t(pair) * P.max_len;
+    int32_t* prow = P.pos_map ? P.pos_map + size_t(pair) * P.max_len : nullptr;
+    auto pool_row = [&](int slot) -> uint32_t {
+      const int phys = __ldg(bt + (slot >> P.page_lg));
+      if (unsigned(phys) >= unsigned(P.num_pages)) {
+        report(P.status, KVSEL_ERR_BAD_INDEX);
+        return kQcNone;
       }
+      return ((uint32_t(phys) * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);   // < 2^31: checked on the host
+    };
+    if (tid < cnt) {
+      const int src = keep[tid];
+      sm.src[tid] = pool_row(src);
+      sm.dst[tid] = pool_row(i0 + tid);
+      sm.cum[tid] = __ldcg(crow + src);
+      if (prow) sm.pos[tid] = __ldcg(prow + src);
     }
     __syncthreads();
-    auto start = [&](int k) {   // round k's rows come into shared memory
-      int i0;
-      const int cnt = share_of(c0 + k * kRound, i0);
-      if (r0 < kStep)
-        for (int i = r0; i < cnt; i += kStep) {
-          const uint32_t row = sm.src[k * kQcRows + i];
-          if (row == kQcNone) continue;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[k & 1][i][w])), "l"(pool + (size_t)row * bytes) : "memory");
-        }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    start(0);
-#pragma unroll 1
-    for (int k = 0; k < rounds; ++k) {
-      // the next round's rows are on their way while this one's are written: they lie behind every
-      // slot that this round writes
-      if (k + 1 < rounds) {
-        start(k + 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (r0 < kStep)
+      for (int i = r0; i < cnt; i += kStep) {
+        const uint32_t row = sm.src[i];
+        if (row == kQcNone) continue;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[i][w])), "l"(pool + (size_t)row * bytes) : "memory");
       }
-      // all of the round's sources are in shared memory before any of its slots is written (what a CTA
-      // reads it has when it arrives, so the barrier need not order memory)
-      asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-      int i0;
-      const int cnt = share_of(c0 + k * kRound, i0);
-      __syncthreads();   // the other threads' copies
-      if (r0 < kStep)
-        for (int i = r0; i < cnt; i += kStep) {
-          const uint32_t row = sm.dst[k * kQcRows + i];
-          if (row == kQcNone || sm.src[k * kQcRows + i] == kQcNone) continue;
-          *reinterpret_cast<uint4*>(pool + (size_t)row * bytes) = sm.unit[k & 1][i][w];
-        }
-      for (int i = tid; i < cnt; i += kQcThreads) {
-        crow[i0 + i] = sm.cum[k * kQcRows + i];
-        if (prow) prow[i0 + i] = sm.pos[k * kQcRows + i];
-      }
-      __syncthreads();   // the stage is free for the round after the next
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // This chunk has been read.  Its slots may be written once every chunk before it has been read too: kept lists
+    // ascend, so keep[i] >= i and only they can have sources there.  A chunk says so before it waits, and chunks are
+    // claimed in order, so whatever is waited for is under way.
+    volatile uint32_t* read = P.read + size_t(pair) * P.chunks;
+    if (tid == 0) {
+      __threadfence();
+      read[k] = 1u;
     }
+    bool go = k == 0;
+#pragma unroll 1
+    for (unsigned spin = 0; !go && spin < limit; ++spin) {
+      const uint32_t from = *(volatile uint32_t*)(P.prefix + pair);
+      bool all = true;
+      for (uint32_t j = from + tid; j < k; j += kQcThreads) all &= read[j] != 0u;
+      // a wait that ran out elsewhere ends this one too (every thread leaves, or none)
+      if (__syncthreads_or(tid == 0 && *(volatile int*)P.status == KVSEL_ERR_TIMEOUT)) break;
+      go = __syncthreads_and(all);
+      if (!go) __nanosleep(100);
+    }
+    if (!go) {   // the same in every thread
+      if (tid == 0) report(P.status, KVSEL_ERR_TIMEOUT);
+      break;
+    }
+    __threadfence();
+    if (tid == 0) atomicMax(P.prefix + pair, k + 1);
+    if (r0 < kStep)
+      for (int i = r0; i < cnt; i += kStep) {
+        const uint32_t row = sm.dst[i];
+        if (row == kQcNone || sm.src[i] == kQcNone) continue;
+        *reinterpret_cast<uint4*>(pool + (size_t)row * bytes) = sm.unit[i][w];
+      }
+    if (tid < cnt) {
+      crow[i0 + tid] = sm.cum[tid];
+      if (prow) prow[i0 + tid] = sm.pos[tid];
+    }
+    __syncthreads();
   }
 }
 
@@ -412,20 +420,28 @@ void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, i
   P.chunk = row_chunk((long long)total * kv->num_kv_heads);
 }
 
+constexpr int kLongRow = 65536;   // rows that may be longer are selected by many CTAs each
+
 struct Evict4Ws {
-  H2OLink link;
-  size_t link_off, keep_off, first_off, total;
+  size_t link_off, keep_off, first_off, long_off, sync_off, sync_bytes, total;
+  int chunks;
 };
 // The status block, then the thresholds and candidate counts of the select
-// (no candidate lists: the 4-bit decode step does not collect any), the kept
-// slots and each row's first slot that moves.
+// (no candidate lists: the 4-bit decode step does not collect any), what the
+// selection of long rows counts in, the kept
+// slots, each row's first slot that moves, and what the chunks of the move
+// synchronise on (the ticket, a prefix per row, a word per chunk).
 Evict4Ws evict4_layout(int batch, int Hkv, int budget) {
   Evict4Ws w;
   const size_t words = align_up(size_t(batch) * Hkv * 4, 256);
   w.link_off = kStatusBytes;
   w.keep_off = w.link_off + 2 * words;
   w.first_off = align_up(w.keep_off + size_t(batch) * Hkv * budget * 4, 256);
-  w.total = w.first_off + words;
+  w.chunks = (budget - 1) / kQcRows + 1;
+  w.long_off = w.first_off + words;
+  w.sync_off = w.long_off + h2o_long_bytes(batch * Hkv);
+  w.sync_bytes = 256 + words + align_up(size_t(batch) * Hkv * w.chunks * 4, 256);
+  w.total = w.sync_off + w.sync_bytes;
   return w;
 }
 
@@ -516,6 +532,8 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
                 fn + "block_table, seq_lens, h2o_cum required; 1 <= batch <= 65535; max_pages, max_len >= 1");
   if (budget < 1 || n_sink < 0 || window < 0 || (long long)n_sink + window > budget)
     return fail(KVSEL_ERR_INVALID_ARG, fn + "need budget >= 1, n_sink >= 0, window >= 0, n_sink + window <= budget");
+  if ((long long)batch * kv->num_kv_heads * ((budget - 1ll) / kQcRows + 1) >= (1ll << 31) - (1 << 20))
+    return fail(KVSEL_ERR_UNSUPPORTED, fn + "batch * num_kv_heads * budget is too large");
   if (!workspace || !aligned(workspace, 256))
     return fail(KVSEL_ERR_INVALID_ARG, fn + "a 256-byte aligned workspace is required");
   const Evict4Ws L = evict4_layout(batch, kv->num_kv_heads, budget);
@@ -540,7 +558,15 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   A.budget = budget;
   A.n_sink = n_sink;
   A.window = window;
-  if (kvsel_status s = launch_h2o_select("kvsel_kv4_evict", A, st); s != KVSEL_OK) return s;
+  if (compact) {   // before the select, which the move follows closely
+    cudaError_t e = cudaMemsetAsync(ws + L.sync_off, 0, L.sync_bytes, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (clear)");
+  }
+  // One CTA a row up to 64K slots (31 us at 32K); beyond, where it takes 1.2 us per 1K slots, a row over many.
+  const bool long_rows = max_len > kLongRow && batch * kv->num_kv_heads <= 65535;
+  const kvsel_status sel = long_rows ? launch_h2o_select_long("kvsel_kv4_evict", A, ws + L.long_off, st)
+                                     : launch_h2o_select("kvsel_kv4_evict", A, st);
+  if (sel != KVSEL_OK) return sel;
   if (!compact) return KVSEL_OK;
 
   Compact4Params C;
@@ -561,23 +587,25 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   C.num_pages = kv->num_pages;
   C.budget = budget;
   C.page_lg = 4 + page_shift_of(kv->page_size);
+  C.batch = batch;
+  C.chunks = L.chunks;
+  C.ticket = reinterpret_cast<uint32_t*>(ws + L.sync_off);
+  C.prefix = reinterpret_cast<uint32_t*>(ws + L.sync_off + 256);
+  C.read = C.prefix + align_up(size_t(batch) * kv->num_kv_heads * 4, 256) / 4;
   if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(sizeof(Compact4Smem)));
       e != cudaSuccess)
     return cuda_fail(e, "kvsel_kv4_evict (attribute)");
-  cudaLaunchAttribute attr[2];
+  const long long total = (long long)batch * kv->num_kv_heads * L.chunks, most = (long long)sm_count() * kQcCtas;
+  cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(kv->num_kv_heads) * kQcCluster, batch);
+  cfg.gridDim = dim3(unsigned(total < most ? total : most));
   cfg.blockDim = dim3(kQcThreads);
   cfg.dynamicSmemBytes = sizeof(Compact4Smem);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kQcCluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   trace_before("kv4_compact", st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_compact_kernel, C);
   trace_after(st);

@@ -93,13 +93,13 @@ KVSEL_API kvsel_status kvsel_read_status(void* workspace, void* stream);
 
 /* Bound the waits on other CTAs of the kernels that use `workspace` (the
  * decode step's per-pair readiness counters, the block-priority sort's grid
- * barriers) at `spins` short sleeps (tens of ns each) instead of the default
+ * barriers, the 4-bit eviction's wait for the chunks before its own) at `spins` short sleeps (tens of ns each) instead of the default
  * of a few seconds; 0 restores the default.  Enqueued on `stream`; the value
  * sits in the workspace's status block and stays until changed or the
  * workspace is zeroed.  A wait that runs out records KVSEL_ERR_TIMEOUT and
  * the kernel finishes without hanging: the decode step's results are then
  * unspecified (every access stays in bounds), the sort stops before its
- * scatter.  Waits inside one CTA (TMA stages) keep their own fixed bound.
+ * scatter, the eviction leaves the rest of the rows unmoved.  Waits inside one CTA (TMA stages) keep their own fixed bound.
  * Failure-detection tests use a short limit with a wait that nothing ends. */
 KVSEL_API kvsel_status kvsel_set_wait_limit(void* workspace, unsigned spins, void* stream);
 

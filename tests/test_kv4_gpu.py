@@ -502,6 +502,93 @@ def test_evict_keeps_what_the_oracle_keeps(S, budget, sink, window, page, mapped
     c.g.check()
 
 
+def test_evict_of_one_long_row_and_of_many_rows():
+    """More chunks than the grid holds at once, of one row and of many; every kept row arrives whole."""
+    for B, Hkv, S, budget, page in ((1, 1, 160001, 150017, 256), (5, 7, 9000, 6000, 64)):
+        rng = np.random.default_rng(B)
+        pages = (S + page - 1) // page
+        table_np = rng.permutation(B * pages).astype(np.int32).reshape(B, pages)
+        gen = torch.Generator(device="cuda").manual_seed(B)
+        codes = [torch.randint(0, 256, (B * pages, Hkv, page, 64), generator=gen, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.randn(B * pages, Hkv, page, 4, 2, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+        table, seq = ints(table_np), ints([S] * B)
+        cum = torch.rand(B, Hkv, S, generator=gen, device="cuda")
+        pos = torch.arange(S, dtype=torch.int32, device="cuda").expand(B, Hkv, S).contiguous()
+
+        def rows(pool, t, n):
+            return pool[t.long()].transpose(1, 2).flatten(2, 3)[:, :, :n].clone()
+        before, cum0 = [rows(p, table, S) for p in codes + scales], cum.clone()
+        keep = torch.zeros(B, Hkv, budget, dtype=torch.int32, device="cuda")
+        kv = K.paged_kv4(*codes, *scales, Hkv)
+        ws = K.workspace(K.kvsel_kv4_evict_workspace(kv, B, budget))
+        t0 = table.clone()
+        K.kvsel_kv4_evict(kv, table, seq, cum, ws, budget=budget, n_sink=4, window=100, compact=True, pos_map=pos, keep_out=keep)
+        assert K.read_status(ws) == 0 and seq.tolist() == [budget] * B
+        for b in range(B):
+            for h in range(Hkv):
+                want = h2o.h2o_keep(cum0[b, h].cpu().numpy(), S, budget, 4, 100)
+                assert np.array_equal(keep[b, h].cpu().numpy(), want)
+        at = keep.long()
+        for was, pool in zip(before, codes + scales):
+            now = rows(pool, t0, budget)
+            idx = at.view(B, Hkv, budget, *[1] * (was.dim() - 3)).expand(B, Hkv, budget, *was.shape[3:])
+            assert torch.equal(now, was.gather(2, idx))
+        assert torch.equal(cum[:, :, :budget], cum0.gather(2, at)) and torch.equal(pos[:, :, :budget], keep)
+
+
+@pytest.mark.parametrize("S,budget,sink,window", [([70000, 500, 66001, 20, 69999], 4000, 4, 300), ([70000], 69999, 0, 0),
+                                                  ([65537, 70000], 1, 0, 0), ([70000, 3000], 3000, 1000, 2000),
+                                                  ([70000], 30000, 7, 29993), ([69000], 50000, 0, 5)])
+def test_evict_of_rows_in_long_buffers(S, budget, sink, window):
+    """Rows that may exceed 64K slots are selected by many CTAs each: ties, short rows, every budget's edges."""
+    rng = np.random.default_rng(budget)
+    B, Hkv, cap, page = len(S), 2, 70000, 256
+    pages = (cap + page - 1) // page
+    table = ints(rng.permutation(B * pages).reshape(B, pages))
+    codes = [torch.from_numpy(rng.integers(0, 256, (B * pages, Hkv, page, 64), dtype=np.uint8)).cuda() for _ in range(2)]
+    scales = [torch.zeros(B * pages, Hkv, page, 4, 2, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cum_np = np.exp(2 * rng.standard_normal((B, Hkv, cap))).astype(np.float32)
+    cum_np = np.where(rng.random(cum_np.shape) < 0.5, np.floor(cum_np * 2) / 2, cum_np).astype(np.float32)   # many ties
+    cum_np[0, 0] = 1.0                                                                                       # and only ties
+    kv = K.paged_kv4(*codes, *scales, Hkv)
+    g = Guards()
+    ws = g.new((K.kvsel_kv4_evict_workspace(kv, B, budget),), torch.uint8)
+    keep, freed = g.new((B, Hkv, budget), torch.int32, -5), g.new((B, pages), torch.int32, -5)
+    seq, cum = g.like(ints(S)), g.like(torch.from_numpy(cum_np).cuda())
+    rows = codes[0][table.long()].transpose(1, 2).flatten(2, 3).clone()
+    t0 = table.clone()
+    K.kvsel_kv4_evict(kv, table, seq, cum, ws, budget=budget, n_sink=sink, window=window, compact=True, keep_out=keep,
+                      freed_pages=freed)
+    assert K.read_status(ws) == 0 and seq.tolist() == [min(s, budget) for s in S]
+    g.check()
+    now = codes[0][t0.long()].transpose(1, 2).flatten(2, 3)
+    for b in range(B):
+        n = min(S[b], budget)
+        for h in range(Hkv):
+            want = h2o.h2o_keep(cum_np[b, h], S[b], budget, sink, window)
+            assert keep[b, h].tolist() == want.tolist() + [-1] * (budget - n), (b, h)
+            at = torch.from_numpy(want).cuda()
+            assert torch.equal(now[b, h, :n], rows[b, h, at]) and torch.equal(cum[b, h, :n], torch.from_numpy(cum_np[b, h, want]).cuda())
+
+
+def test_evict_whose_wait_may_run_out_ends():
+    """With a wait of one poll the move ends at once, with KVSEL_ERR_TIMEOUT where a chunk was not ready."""
+    rng = np.random.default_rng(2)
+    c = Cache(rng, 2, 2, 2, 16, 4000)
+    ws = K.workspace(K.kvsel_kv4_evict_workspace(c.kv, 2, 3500))
+    cum = torch.rand(2, 2, 4000, device="cuda")
+    K.set_wait_limit(ws, 1)
+    K.kvsel_kv4_evict(c.kv, c.table, ints([4000, 4000]), cum, ws, budget=3500, n_sink=4, window=50, compact=True)
+    assert K.read_status(ws) in (0, K.KVSEL_ERR_TIMEOUT)
+    K.set_wait_limit(ws, 0)
+    c2 = Cache(np.random.default_rng(2), 2, 2, 2, 16, 4000)
+    seq = ints([4000, 4000])
+    K.kvsel_kv4_evict(c2.kv, c2.table, seq, torch.rand(2, 2, 4000, device="cuda"), ws, budget=3500, n_sink=4, window=50, compact=True)
+    assert K.read_status(ws) == 0 and seq.tolist() == [3500, 3500]
+    c.g.check()
+    c2.g.check()
+
+
 def test_evict_reports_what_does_not_fit():
     rng = np.random.default_rng(3)
     c = Cache(rng, 2, 1, 1, 16, 64)
