@@ -8,7 +8,7 @@
 //   read twice and every store is part of a full 64-byte row: 512 bytes read
 //   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
-// evict: the select of h2o_evict.cu, then the kept rows move in chunks of 224,
+// evict: the select of h2o_evict.cu, then the kept rows move in chunks of 448,
 //   claimed by a persistent grid in order.  A chunk comes into shared memory,
 //   says that it has been read, waits until all chunks before it of its
 //   (sequence, kv head) have been read, and is written to its new slots: kept
@@ -16,7 +16,8 @@
 //   there.  Every SM works whether there are 64 rows of 6.5K kept slots or
 //   one of 300K; one CTA per (sequence, kv head), as the bf16 cache's compaction
 //   has it, leaves most of them idle, and a cluster of 8 per (sequence, kv head)
-//   in lock-step rounds took 41 us at 64 x 6.5K and 1 us per 896 rows of one.
+//   in lock-step rounds took 41 us at 64 x 6.5K (this: 48) but 1 us per 896 rows
+//   of one (235K rows: 260 us, this: 38).
 #include "common.cuh"
 #include "h2o_select.cuh"
 #include "kv4.cuh"
@@ -236,9 +237,9 @@ __global__ void __launch_bounds__(kQaThreads) kv4_read_kernel(const ReadParams P
 // ---------------------------------------------------------------------------
 // compaction
 // ---------------------------------------------------------------------------
-constexpr int kQcRows = 224;     // kept rows of a chunk; four CTAs an SM
-constexpr int kQcCtas = 4;
-constexpr int kQcThreads = 256;
+constexpr int kQcRows = 448;     // kept rows of a chunk; two CTAs an SM (four of 224 rows: the same at 64 rows, 1.15 times at one)
+constexpr int kQcCtas = 2;
+constexpr int kQcThreads = 512;
 constexpr int kQcUnits = 10;     // 16-byte units of a row: K codes 4, V codes 4, K and V scales
 constexpr uint32_t kQcNone = 0xFFFFFFFFu;
 constexpr unsigned kQcSpins = 1u << 22;  // polls of the chunks before, each a short sleep: seconds
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
   const int page_mask = (1 << P.page_lg) - 1;
   const uint32_t pairs = uint32_t(P.batch) * P.Hkv, total = pairs * P.chunks;   // < 2^31: checked on the host
-  // thread t moves unit t % 10 of rows t / 10, t / 10 + 25, ... (250 of the 256 threads)
+  // thread t moves unit t % 10 of rows t / 10, t / 10 + 51, ... (510 of the 512 threads)
   const int w = tid % kQcUnits, r0 = tid / kQcUnits;
   constexpr int kStep = kQcThreads / kQcUnits;
   uint8_t* const pool = w < 4 ? P.codes[0] + w * 16 : w < 8 ? P.codes[1] + (w - 4) * 16 : w == 8 ? P.scales[0] : P.scales[1];
@@ -313,12 +314,12 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
       }
       return ((uint32_t(phys) * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);   // < 2^31: checked on the host
     };
-    if (tid < cnt) {
-      const int src = keep[tid];
-      sm.src[tid] = pool_row(src);
-      sm.dst[tid] = pool_row(i0 + tid);
-      sm.cum[tid] = __ldcg(crow + src);
-      if (prow) sm.pos[tid] = __ldcg(prow + src);
+    for (int i = tid; i < cnt; i += kQcThreads) {
+      const int src = keep[i];
+      sm.src[i] = pool_row(src);
+      sm.dst[i] = pool_row(i0 + i);
+      sm.cum[i] = __ldcg(crow + src);
+      if (prow) sm.pos[i] = __ldcg(prow + src);
     }
     __syncthreads();
     if (r0 < kStep)
@@ -360,10 +361,11 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
         if (row == kQcNone || sm.src[i] == kQcNone) continue;
         *reinterpret_cast<uint4*>(pool + (size_t)row * bytes) = sm.unit[i][w];
       }
-    if (tid < cnt) {
-      crow[i0 + tid] = sm.cum[tid];
-      if (prow) prow[i0 + tid] = sm.pos[tid];
+    for (int i = tid; i < cnt; i += kQcThreads) {
+      crow[i0 + i] = sm.cum[i];
+      if (prow) prow[i0 + i] = sm.pos[i];
     }
+    if (gridDim.x >= total) break;   // a chunk a CTA
     __syncthreads();
   }
 }
@@ -420,7 +422,7 @@ void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, i
   P.chunk = row_chunk((long long)total * kv->num_kv_heads);
 }
 
-constexpr int kLongRow = 65536;   // rows that may be longer are selected by many CTAs each
+constexpr int kLongRow = 32768;   // rows that may have more candidates are selected by many CTAs each
 
 struct Evict4Ws {
   size_t link_off, keep_off, first_off, long_off, sync_off, sync_bytes, total;
@@ -562,8 +564,9 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
     cudaError_t e = cudaMemsetAsync(ws + L.sync_off, 0, L.sync_bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (clear)");
   }
-  // One CTA a row up to 64K slots (31 us at 32K); beyond, where it takes 1.2 us per 1K slots, a row over many.
-  const bool long_rows = max_len > kLongRow && batch * kv->num_kv_heads <= 65535;
+  // One CTA a row while it holds a row's scores in registers (27 us at 32K); beyond, where it takes 1.2 us per
+  // 1K slots, a row over many (40 us at 220K to 830K slots).
+  const bool long_rows = (long long)max_len - n_sink - window > kLongRow && batch * kv->num_kv_heads <= 65535;
   const kvsel_status sel = long_rows ? launch_h2o_select_long("kvsel_kv4_evict", A, ws + L.long_off, st)
                                      : launch_h2o_select("kvsel_kv4_evict", A, st);
   if (sel != KVSEL_OK) return sel;
