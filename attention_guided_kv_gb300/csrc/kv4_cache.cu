@@ -8,16 +8,13 @@
 //   read twice and every store is part of a full 64-byte row: 512 bytes read
 //   and 160 written a row.  Where a row goes is looked up by one thread a row.
 // read kernel: the inverse, 160 bytes read and 512 written a row.
-// evict: the select of h2o_evict.cu, then the kept rows move in chunks of 448,
-//   claimed by a persistent grid in order.  A chunk comes into shared memory,
-//   says that it has been read, waits until all chunks before it of its
-//   (sequence, kv head) have been read, and is written to its new slots: kept
-//   lists ascend, so keep[i] >= i and only chunks before it can have sources
-//   there.  Every SM works whether there are 64 rows of 6.5K kept slots or
-//   one of 300K; one CTA per (sequence, kv head), as the bf16 cache's compaction
-//   has it, leaves most of them idle, and a cluster of 8 per (sequence, kv head)
-//   in lock-step rounds took 41 us at 64 x 6.5K (this: 48) but 1 us per 896 rows
-//   of one (235K rows: 260 us, this: 38).
+// evict: the select of h2o_evict.cu (h2o_select_long.cu for long rows), then
+//   the kept rows move through shared memory.  Kept lists ascend, so keep[i] >=
+//   i: a row's new slot can only be a source of rows before it, and may be
+//   written once those have been read.  Up to 7168 kept rows a (sequence, kv
+//   head) a cluster of 8 CTAs does that in lock-step rounds, beyond a persistent
+//   grid in chunks of 448 rows, claimed in order; one CTA per (sequence, kv
+//   head), as the bf16 cache's compaction has it, leaves most SMs idle.
 #include "common.cuh"
 #include "h2o_select.cuh"
 #include "kv4.cuh"
@@ -370,6 +367,121 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
   }
 }
 
+// The move of at most kQkMost kept rows a (sequence, kv head): a cluster of 8 CTAs each, in rounds of 8 x 112 rows.
+// A round's rows come into the cluster's shared memory, the cluster waits for all of them and writes them; the next
+// round's rows load meanwhile.  64 rows of 32K to 6.5K kept slots: 41 us, against 48 for the chunks above; from 10K
+// kept slots on the chunks win, as only 8 CTAs work on a row here (235K rows of one: 260 us against 38).
+constexpr int kQkCluster = 8;
+constexpr int kQkRows = 112;     // kept rows a CTA stages per round; four CTAs an SM
+constexpr int kQkRounds = 8;
+constexpr int kQkThreads = 256;
+constexpr int kQkMost = kQkCluster * kQkRows * kQkRounds;
+
+struct ClusterSmem {
+  uint4 unit[2][kQkRows][kQcUnits];
+  uint32_t src[kQkRounds * kQkRows], dst[kQkRounds * kQkRows];  // pool rows, kQcNone: a bad table entry
+  float cum[kQkRounds * kQkRows];
+  int32_t pos[kQkRounds * kQkRows];
+};
+
+__global__ void __launch_bounds__(kQkThreads) kv4_compact_cluster_kernel(const Compact4Params P) {
+  extern __shared__ __align__(16) uint8_t qc_smem[];
+  ClusterSmem& sm = *reinterpret_cast<ClusterSmem*>(qc_smem);
+  const int rank = blockIdx.x % kQkCluster, kvh = blockIdx.x / kQkCluster, b = blockIdx.y, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kept lists come from the select
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the truncation waits for this kernel
+  const int S = P.seq_lens[b];
+  if (S <= P.budget) return;  // the same for the whole cluster, as below
+  if (S > P.max_len || (long long)S > ((long long)P.max_pages << P.page_lg)) {
+    if (tid == 0) report(P.status, KVSEL_ERR_BAD_INDEX);
+    return;
+  }
+  const size_t rowi = size_t(b) * P.Hkv + kvh;
+  const int32_t* keep = P.keep_slots + rowi * P.budget;
+  const int32_t* bt = P.block_table + size_t(b) * P.max_pages;
+  float* crow = P.cum + rowi * P.max_len;
+  int32_t* prow = P.pos_map ? P.pos_map + rowi * P.max_len : nullptr;
+  const int page_mask = (1 << P.page_lg) - 1;
+  auto pool_row = [&](int slot) -> uint32_t {
+    const int phys = __ldg(bt + (slot >> P.page_lg));
+    if (unsigned(phys) >= unsigned(P.num_pages)) {
+      report(P.status, KVSEL_ERR_BAD_INDEX);
+      return kQcNone;
+    }
+    return ((uint32_t(phys) * P.Hkv + kvh) << P.page_lg) + (slot & page_mask);   // < 2^31: checked on the host
+  };
+  // This CTA's rows of the round that starts at c0: an even share for every CTA of the cluster.
+  auto share_of = [&](int c0, int& i0) {
+    const int left = min(kQkCluster * kQkRows, P.budget - c0);
+    const int share = (left + kQkCluster - 1) / kQkCluster;
+    i0 = c0 + rank * share;
+    return max(0, min(share, left - rank * share));
+  };
+  // thread t moves unit t % 10 of rows t / 10, t / 10 + 25, ... (250 of the 256 threads)
+  const int w = tid % kQcUnits, r0 = tid / kQcUnits;
+  constexpr int kStep = kQkThreads / kQcUnits;
+  uint8_t* const pool = w < 4 ? P.codes[0] + w * 16 : w < 8 ? P.codes[1] + (w - 4) * 16 : w == 8 ? P.scales[0] : P.scales[1];
+  const uint32_t bytes = w < 8 ? kQ4CodeBytes : kQ4ScaleBytes;
+  constexpr int kRound = kQkCluster * kQkRows;
+  const int c0 = P.first_move[rowi];
+  if (c0 < P.budget) {
+    const int rounds = (P.budget - c0 + kRound - 1) / kRound;   // at most kQkRounds: the host's rule
+    // where the rows come from and go to
+    for (int x = tid; x < rounds * kQkRows; x += kQkThreads) {
+      const int k = x / kQkRows, i = x - k * kQkRows;
+      int i0;
+      if (i < share_of(c0 + k * kRound, i0)) {
+        const int src = keep[i0 + i];
+        sm.src[x] = pool_row(src);
+        sm.dst[x] = pool_row(i0 + i);
+        sm.cum[x] = crow[src];
+        if (prow) sm.pos[x] = prow[src];
+      }
+    }
+    __syncthreads();
+    auto start = [&](int k) {   // round k's rows come into shared memory
+      int i0;
+      const int cnt = share_of(c0 + k * kRound, i0);
+      if (r0 < kStep)
+        for (int i = r0; i < cnt; i += kStep) {
+          const uint32_t row = sm.src[k * kQkRows + i];
+          if (row == kQcNone) continue;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.unit[k & 1][i][w])), "l"(pool + (size_t)row * bytes) : "memory");
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    start(0);
+#pragma unroll 1
+    for (int k = 0; k < rounds; ++k) {
+      // the next round's rows are on their way while this one's are written: they lie behind every
+      // slot that this round writes
+      if (k + 1 < rounds) {
+        start(k + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      // all of the round's sources are in shared memory before any of its slots is written (what a CTA
+      // reads it has when it arrives, so the barrier need not order memory)
+      asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+      int i0;
+      const int cnt = share_of(c0 + k * kRound, i0);
+      __syncthreads();   // the other threads' copies
+      if (r0 < kStep)
+        for (int i = r0; i < cnt; i += kStep) {
+          const uint32_t row = sm.dst[k * kQkRows + i];
+          if (row == kQcNone || sm.src[k * kQkRows + i] == kQcNone) continue;
+          *reinterpret_cast<uint4*>(pool + (size_t)row * bytes) = sm.unit[k & 1][i][w];
+        }
+      for (int i = tid; i < cnt; i += kQkThreads) {
+        crow[i0 + i] = sm.cum[k * kQkRows + i];
+        if (prow) prow[i0 + i] = sm.pos[k * kQkRows + i];
+      }
+      __syncthreads();   // the stage is free for the round after the next
+    }
+  }
+}
+
 }  // namespace kvsel
 
 using namespace kvsel;
@@ -560,7 +672,8 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   A.budget = budget;
   A.n_sink = n_sink;
   A.window = window;
-  if (compact) {   // before the select, which the move follows closely
+  const bool clusters = budget <= kQkMost;
+  if (compact && !clusters) {   // before the select, which the move follows closely
     cudaError_t e = cudaMemsetAsync(ws + L.sync_off, 0, L.sync_bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (clear)");
   }
@@ -595,22 +708,26 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
   C.ticket = reinterpret_cast<uint32_t*>(ws + L.sync_off);
   C.prefix = reinterpret_cast<uint32_t*>(ws + L.sync_off + 256);
   C.read = C.prefix + align_up(size_t(batch) * kv->num_kv_heads * 4, 256) / 4;
-  if (cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kv4_compact_kernel), int(sizeof(Compact4Smem)));
-      e != cudaSuccess)
-    return cuda_fail(e, "kvsel_kv4_evict (attribute)");
+  const void* fnp = clusters ? reinterpret_cast<const void*>(kv4_compact_cluster_kernel) : reinterpret_cast<const void*>(kv4_compact_kernel);
+  const size_t smem = clusters ? sizeof(ClusterSmem) : sizeof(Compact4Smem);
+  if (cudaError_t e = smem_limit_once(fnp, int(smem)); e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (attribute)");
   const long long total = (long long)batch * kv->num_kv_heads * L.chunks, most = (long long)sm_count() * kQcCtas;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(total < most ? total : most));
-  cfg.blockDim = dim3(kQcThreads);
-  cfg.dynamicSmemBytes = sizeof(Compact4Smem);
+  cfg.gridDim = clusters ? dim3(unsigned(kv->num_kv_heads) * kQkCluster, batch) : dim3(unsigned(total < most ? total : most));
+  cfg.blockDim = dim3(clusters ? kQkThreads : kQcThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kQkCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = clusters ? 2 : 1;
   trace_before("kv4_compact", st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_compact_kernel, C);
+  cudaError_t e = clusters ? cudaLaunchKernelEx(&cfg, kv4_compact_cluster_kernel, C) : cudaLaunchKernelEx(&cfg, kv4_compact_kernel, C);
   trace_after(st);
   if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (compact launch)");
 
