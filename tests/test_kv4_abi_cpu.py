@@ -116,6 +116,7 @@ def test_evict(lib):
                 dict(max_len=0), dict(budget=0), dict(budget=7), dict(sink=-1), dict(window=-1), dict(ws=None),
                 dict(ws=8), dict(ws_bytes=64)):
         assert _evict(lib, **bad) == INV, bad
+    assert _evict(lib, batch=65535, budget=(1 << 31) - 1, sink=0, window=0, max_len=(1 << 31) - 1) == UNS
     need = K.kvsel_kv4_evict_workspace(_kv(), 2, 10)
     assert need >= 256 + 2 * 8 * 10 * 4
     assert _evict(lib, ws_bytes=need - 1) == INV
