@@ -736,7 +736,6 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
   if (chunk < 0) {
     const int head = blockIdx.x;
     float mx = -INFINITY;
-#pragma unroll 4
     for (int i = tid; i < n_part; i += kQfThreads) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -747,7 +746,6 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     const float use = mx == -INFINITY ? 0.f : mx;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float lsum = 0.f;
-#pragma unroll 4
     for (int i = warp; i < n_part; i += kQfThreads / 32) {
       const float2 ml = __ldcg(&P.part_ml[(first + i) * P.G + head]);
       const float f = ex2(ml.x - use);
@@ -811,7 +809,6 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
     }
     float mx = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
     if (head < P.G)
-#pragma unroll 6
       for (int i = l16 + 64; i < n_part; i += 16) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
 #pragma unroll
     for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -820,7 +817,6 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum = fmaf(ml[k].y, ex2(ml[k].x - use), sum);
     if (head < P.G)
-#pragma unroll 6
       for (int i = l16 + 64; i < n_part; i += 16) {
         const float2 v = __ldcg(&P.part_ml[(first + i) * P.G + head]);
         sum = fmaf(v.y, ex2(v.x - use), sum);
