@@ -797,30 +797,50 @@ __global__ void __launch_bounds__(kQfThreads) kv4_finalize_kernel(const Decode4P
         v[h][k] = use[k] && h0 + h < P.G ? __ldcs(lg + (size_t)(h0 + h) * P.max_len + s0 + k * kQfThreads) : -INFINITY;
   };
   load(0);   // on their way while the statistics are joined
-  // every head's maximum and 1 / sum: 16 threads a head, the first 4 partials of each read at once
+  // every head's maximum and 1 / sum: 16 threads a head.  Up to 64 partials are read at once; more of them 6 a thread at
+  // a time, with a running maximum, as one read after another waits for memory each time.
   {
     const int head = tid >> 4, l16 = tid & 15;
-    float2 ml[4];
+    float mx = -INFINITY, use, sum = 0.f;
+    if (n_part <= 64) {
+      float2 ml[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = l16 + 16 * k;
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (head < P.G && i < n_part) ml[k] = __ldcg(&P.part_ml[(first + i) * P.G + head]);
-    }
-    float mx = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-    if (head < P.G)
-      for (int i = l16 + 64; i < n_part; i += 16) mx = fmaxf(mx, __ldcg(&P.part_ml[(first + i) * P.G + head]).x);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float use = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum = fmaf(ml[k].y, ex2(ml[k].x - use), sum);
-    if (head < P.G)
-      for (int i = l16 + 64; i < n_part; i += 16) {
-        const float2 v = __ldcg(&P.part_ml[(first + i) * P.G + head]);
-        sum = fmaf(v.y, ex2(v.x - use), sum);
+      for (int k = 0; k < 4; ++k) {
+        const int i = l16 + 16 * k;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (head < P.G && i < n_part) ml[k] = __ldcg(&P.part_ml[(first + i) * P.G + head]);
       }
+      mx = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      use = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum = fmaf(ml[k].y, ex2(ml[k].x - use), sum);
+    } else {
+      if (head < P.G)
+#pragma unroll 1
+        for (int i0 = l16; i0 < n_part; i0 += 16 * 6) {
+          float2 ml[6];
+#pragma unroll
+          for (int k = 0; k < 6; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i0 + 16 * k < n_part) ml[k] = __ldcg(&P.part_ml[(first + i0 + 16 * k) * P.G + head]);
+          }
+          float top = mx;
+#pragma unroll
+          for (int k = 0; k < 6; ++k) top = fmaxf(top, ml[k].x);
+          const float ref = top == -INFINITY ? 0.f : top;
+          sum *= ex2(mx - ref);
+#pragma unroll
+          for (int k = 0; k < 6; ++k) sum = fmaf(ml[k].y, ex2(ml[k].x - ref), sum);
+          mx = top;
+        }
+      float top = mx;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      use = top == -INFINITY ? 0.f : top;
+      sum *= ex2(mx - use);
+    }
 #pragma unroll
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (l16 == 0) {
