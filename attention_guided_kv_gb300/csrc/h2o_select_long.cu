@@ -1,7 +1,8 @@
 // H2O selection of long rows (sm_103a): the keep lists of h2o_select_kernel
 // (h2o_evict.cu), with a row spread over many CTAs.
 //
-// One CTA per row reads 830K scores at the pace of one SM (about 1 ms; this: 40 us); here a
+// One CTA per row reads 830K scores at the pace of one SM (1005 us; this: 66, events
+// around its five launches); here a
 // row's candidate slots [n_sink, S - window) are cut into slices, one CTA each:
 //   hist kernel, three passes: counts of the order keys' digits (11, 11 and 10
 //     bits, from the top), each pass among the keys that share the digits found
@@ -289,7 +290,7 @@ kvsel_status launch_h2o_select_long(const char* fn, const H2OSelectArgs& a, void
   P.n_sink = a.n_sink;
   P.window = a.window;
   const int want = 4 * sm_count() / rows;   // four CTAs an SM
-  P.slices = want < 8 ? 8 : want > kMostSlices ? kMostSlices : want;
+  P.slices = want < 1 ? 1 : want > kMostSlices ? kMostSlices : want;
   cudaError_t e = cudaMemsetAsync(P.hist, 0, size_t(rows) * 3 * kHlBins * sizeof(uint32_t), st);
   if (e != cudaSuccess) return cuda_fail(e, (name + " (clear)").c_str());
   cudaLaunchAttribute attr[1];

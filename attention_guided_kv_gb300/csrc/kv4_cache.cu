@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(kQcThreads) kv4_compact_kernel(const Compact4P
 
 // The move of at most kQkMost kept rows a (sequence, kv head): a cluster of 8 CTAs each, in rounds of 8 x 112 rows.
 // A round's rows come into the cluster's shared memory, the cluster waits for all of them and writes them; the next
-// round's rows load meanwhile.  64 rows of 32K to 6.5K kept slots: 41 us, against 48 for the chunks above; from 10K
-// kept slots on the chunks win, as only 8 CTAs work on a row here (235K rows of one: 260 us against 38).
+// round's rows load meanwhile.  64 rows of 32K to 6.5K kept slots: 46.6 us, against 52.8 for the chunks above; of
+// 235K kept slots of one row 430 against 41, of 124K of four rows 241 against 59, as only 8 CTAs work on a row here
+// (events around the launch).  Between 7168, what a CTA notes the places of at once, and 124K it is not measured.
 constexpr int kQkCluster = 8;
 constexpr int kQkRows = 112;     // kept rows a CTA stages per round; four CTAs an SM
 constexpr int kQkRounds = 8;
@@ -534,7 +535,15 @@ void fill(Kv4Params& P, const kvsel_paged_kv4* kv, const int32_t* block_table, i
   P.chunk = row_chunk((long long)total * kv->num_kv_heads);
 }
 
-constexpr int kLongRow = 32768;   // rows that may have more candidates are selected by many CTAs each
+// Whether a selection spreads each row over many CTAs.  Whole evictions to 6553 slots, many CTAs a row / one: 1 row of
+// 34K slots 64 / 84 us, of 200K 86 / 163; 2 of 34K 72 / 84; 8 of 34K 104 / 96, of 66K 112 / 106, of 200K 131 / 180; 32 of
+// 66K 150 / 142, of 200K 206 / 229; 64 of 200K 344 / 307; 128 of 66K 376 / 297.  (3 rows, and more than 64 rows of more than
+// 66K or 64 of more than 200K, are not measured.)
+constexpr int kLongRow = 32768, kLongRowMany = 100000;   // candidates; the second for more than kLongFew rows
+constexpr int kLongFew = 2, kLongRows = 32;
+static bool spread_rows(long long candidates, int rows) {
+  return rows <= kLongRows && candidates > (rows <= kLongFew ? kLongRow : kLongRowMany);
+}
 
 struct Evict4Ws {
   size_t link_off, keep_off, first_off, long_off, sync_off, sync_bytes, total;
@@ -553,7 +562,7 @@ Evict4Ws evict4_layout(int batch, int Hkv, int budget) {
   w.first_off = align_up(w.keep_off + size_t(batch) * Hkv * budget * 4, 256);
   w.chunks = (budget - 1) / kQcRows + 1;
   w.long_off = w.first_off + words;
-  w.sync_off = w.long_off + h2o_long_bytes(batch * Hkv);
+  w.sync_off = w.long_off + (batch * Hkv <= kLongRows ? h2o_long_bytes(batch * Hkv) : 0);
   w.sync_bytes = 256 + words + align_up(size_t(batch) * Hkv * w.chunks * 4, 256);
   w.total = w.sync_off + w.sync_bytes;
   return w;
@@ -677,9 +686,7 @@ extern "C" kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* bloc
     cudaError_t e = cudaMemsetAsync(ws + L.sync_off, 0, L.sync_bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, "kvsel_kv4_evict (clear)");
   }
-  // One CTA a row while it holds a row's scores in registers (27 us at 32K); beyond, where it takes 1.2 us per
-  // 1K slots, a row over many (40 us at 220K to 830K slots).
-  const bool long_rows = (long long)max_len - n_sink - window > kLongRow && batch * kv->num_kv_heads <= 65535;
+  const bool long_rows = spread_rows((long long)max_len - n_sink - window, batch * kv->num_kv_heads);
   const kvsel_status sel = long_rows ? launch_h2o_select_long("kvsel_kv4_evict", A, ws + L.long_off, st)
                                      : launch_h2o_select("kvsel_kv4_evict", A, st);
   if (sel != KVSEL_OK) return sel;

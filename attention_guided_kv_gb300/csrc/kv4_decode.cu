@@ -33,7 +33,7 @@
 //   unpacked by 8 lanes (the first form of this kernel took 119 us instead of
 //   88 us at 8 x 32K, 64/8 heads).  p s turns into the second product's layout
 //   with movmatrix.  mma.sync, not tcgen05: with at most 16 columns of q the
-//   product is a sixth of what the warp-level instruction can do, and the
+//   product takes 24 % of the tensor pipe's cycles (8 x 32K), and the
 //   codes reach it from registers.
 //   A warp whose share ends inside a pair leaves its m, l and partial output.
 // finalize kernel: joins the partials of each pair (one CTA per q head), turns

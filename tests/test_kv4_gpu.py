@@ -428,6 +428,13 @@ def test_decode_many_warps_share_a_row():
     _decode_case(1, 8, 16, [40] * 100, seed=13)
 
 
+@pytest.mark.parametrize("S", [2048, 2080, 3100, 3600, 9000])
+@pytest.mark.parametrize("G,window", [(1, 0), (8, 0), (3, 40), (16, 1)])
+def test_decode_joins_few_and_many_partials(S, G, window):
+    """Around 64 and 96 partials, with windows that leave most of them empty."""
+    _decode_case(G, 1, 64, [S], seed=S + G, append=False, window=window, n_sink=2 if window else 0)
+
+
 def test_decode_reports_lengths_and_pages_that_do_not_fit():
     rng = np.random.default_rng(14)
     c = Cache(rng, 3, 2, 4, 16, 64)
@@ -569,6 +576,43 @@ def test_evict_of_rows_in_long_buffers(S, budget, sink, window):
             assert keep[b, h].tolist() == want.tolist() + [-1] * (budget - n), (b, h)
             at = torch.from_numpy(want).cuda()
             assert torch.equal(now[b, h, :n], rows[b, h, at]) and torch.equal(cum[b, h, :n], torch.from_numpy(cum_np[b, h, want]).cuda())
+
+
+@pytest.mark.parametrize("B,Hkv,cap", [(1, 2, 33000), (1, 3, 99000), (1, 3, 101000), (4, 8, 101000), (3, 11, 101000)])
+def test_evict_selects_the_same_however_a_row_is_spread(B, Hkv, cap):
+    """Rows on both sides of the rule that spreads a row over many CTAs, full ones and short ones."""
+    rng = np.random.default_rng(cap + B)
+    budget, sink, window, page = 500, 4, 60, 16
+    kv = K.paged_kv4(*[torch.zeros(B, Hkv, page, 64, dtype=torch.uint8, device="cuda") for _ in range(2)],
+                     *[torch.zeros(B, Hkv, page, 4, 2, dtype=torch.bfloat16, device="cuda") for _ in range(2)], Hkv)
+    pages = (cap + page - 1) // page
+    cum_np = rng.random((B, Hkv, cap)).astype(np.float32)
+    cum_np[..., ::7] = 0.9975                                  # ties, which the long rows' last kept scores are among
+    S = [cap if b % 2 == 0 else 900 + b for b in range(B)]
+    g = Guards()
+    ws = g.new((K.kvsel_kv4_evict_workspace(kv, B, budget),), torch.uint8)
+    keep, seq, cum = g.new((B, Hkv, budget), torch.int32, -5), g.like(ints(S)), g.like(torch.from_numpy(cum_np).cuda())
+    K.kvsel_kv4_evict(kv, torch.zeros(B, pages, dtype=torch.int32, device="cuda"), seq, cum, ws, budget=budget, n_sink=sink,
+                      window=window, compact=False, keep_out=keep)
+    assert K.read_status(ws) == 0 and seq.tolist() == S
+    g.check()
+    for b in range(B):
+        for h in range(Hkv):
+            assert keep[b, h].tolist() == h2o.h2o_keep(cum_np[b, h], S[b], budget, sink, window).tolist(), (b, h)
+
+
+def test_evict_in_chunks_whose_wait_may_run_out_ends():
+    """As below, with more kept rows than the clusters move."""
+    for limit in (1, 0):
+        c = Cache(np.random.default_rng(2), 2, 2, 2, 16, 9000)
+        ws = K.workspace(K.kvsel_kv4_evict_workspace(c.kv, 2, 8000))
+        seq = ints([9000, 9000])
+        K.set_wait_limit(ws, limit)
+        K.kvsel_kv4_evict(c.kv, c.table, seq, torch.rand(2, 2, 9000, device="cuda"), ws, budget=8000, n_sink=4, window=50, compact=True)
+        assert K.read_status(ws) in ((0, K.KVSEL_ERR_TIMEOUT) if limit else (0,))
+        if not limit:
+            assert seq.tolist() == [8000, 8000]
+        c.g.check()
 
 
 def test_evict_whose_wait_may_run_out_ends():
