@@ -562,7 +562,7 @@ Evict4Ws evict4_layout(int batch, int Hkv, int budget) {
   w.first_off = align_up(w.keep_off + size_t(batch) * Hkv * budget * 4, 256);
   w.chunks = (budget - 1) / kQcRows + 1;
   w.long_off = w.first_off + words;
-  w.sync_off = w.long_off + (batch * Hkv <= kLongRows ? h2o_long_bytes(batch * Hkv) : 0);
+  w.sync_off = w.long_off + ((long long)batch * Hkv <= kLongRows ? h2o_long_bytes(batch * Hkv) : 0);
   w.sync_bytes = 256 + words + align_up(size_t(batch) * Hkv * w.chunks * 4, 256);
   w.total = w.sync_off + w.sync_bytes;
   return w;

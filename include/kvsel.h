@@ -776,8 +776,8 @@ KVSEL_API kvsel_status kvsel_kv4_decode_attn(const kvsel_paged_kv4* kv, const in
  * codes and scales moved as they are (nothing is requantised).
  *   workspace    >= kvsel_kv4_evict_workspace() bytes, zeroed before first use;
  *                kvsel_h2o_link_reset applies to it.
- * Launches: select (five for few long rows), and
- * with compact != 0 move and truncate. */
+ * Launches: select (five for few long rows), and with compact != 0 move and
+ * truncate. */
 KVSEL_API size_t kvsel_kv4_evict_workspace(const kvsel_paged_kv4* kv, int batch, int budget);
 KVSEL_API kvsel_status kvsel_kv4_evict(const kvsel_paged_kv4* kv, int32_t* block_table, int max_pages, int32_t* seq_lens,
                                        int batch, float* h2o_cum, int32_t* pos_map, int max_len, int budget, int n_sink,

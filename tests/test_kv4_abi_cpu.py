@@ -153,3 +153,11 @@ def test_prefill(lib):
     assert st(ws_bytes=K.kvsel_prefill_attn_workspace(kv, 2, 9) - 1) == INV
     assert K.kvsel_prefill_attn_workspace(kv, 0, 9) == 0
     assert st(total=0, q=None, out=None) == K.KVSEL_OK
+
+
+def test_evict_workspace_of_many_rows_does_not_wrap():
+    """Six words a (sequence, kv head) at a budget of one, also where their number passes 2^31 (whole 256-byte blocks here)."""
+    def size(batch):
+        return K.kvsel_kv4_evict_workspace(_kv(), batch, 1)
+    for batch in (72, 1 << 20, (1 << 31) - 8):
+        assert size(batch) - size(64) == 24 * 8 * (batch - 64), batch
